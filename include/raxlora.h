@@ -422,6 +422,172 @@ lora_status lora_route_embedding(const lora_pool* pool, lora_routing* routing, c
                                  const int32_t* vocab_ids, void* y, int ldy, lora_dtype ydtype, hipStream_t stream);
 
 /*
+ * ---- Between the packed q/k/v projection and the o projection of a layer ----
+ *
+ * The page plan, the rotary append and the paged attention below take a step from the
+ * packed q/k/v rows (base output plus lora_linear's correction) to the attention output
+ * that the o projection reads.  They share one paged cache: keys and values lie in pages
+ * of page_size tokens, a sequence's block table names its pages in order, and a token's
+ * slot is page * page_size + offset within the page.  Conventions as above; in addition:
+ *   - page_size is a power of two from 16 to 1024 and num_pages * page_size < 2^31.
+ *   - Ids, lengths, positions and slots are int32 device vectors.  Page ids and slots
+ *     outside the cache are never followed: a token with such a slot is not stored, the
+ *     keys of such a page are left out of the attention.
+ */
+#define LORA_MAX_SEQS      4096   /* sequences of one step */
+#define LORA_MAX_HEAD_DIM  256
+#define LORA_PLAN_META     8      /* words of lora_page_plan's meta */
+
+/*
+ * One layer's paged cache, the caller's memory.  Element i of the key (value) of kv head h
+ * at offset o of page p lies at k (v) + p * page_stride + o * token_stride + h *
+ * head_stride + i, strides in elements, the same for k and v: [page][offset][head][i] and
+ * [page][head][offset][i] are both possible.  dtype LORA_BF16, LORA_F32 or LORA_FP8E4M3;
+ * an e4m3 cache stands for its values times k_scale (keys) and v_scale (values), which are
+ * positive and finite (ignored for the other types).  Rules, checked by the calls:
+ * head_dim a multiple of 16 up to LORA_MAX_HEAD_DIM (SHAPE above it, else ALIGN), strides
+ * multiples of 16, below 2^25 for token_stride, large enough that no two elements share
+ * an address (SHAPE), k and v 16-byte aligned (ALIGN).
+ */
+typedef struct lora_kv_cache {
+  void* k;
+  void* v;
+  int64_t page_stride, token_stride, head_stride;
+  int32_t num_pages, page_size, num_heads, head_dim;
+  int32_t dtype;
+  float k_scale, v_scale;
+} lora_kv_cache;
+
+/*
+ * Block table, slot map and positions of one step, from the request lengths, with the
+ * pages themselves taken from and given back to a ring of free pages, all on the GPU.
+ * Request r has past_lens[r] tokens in the cache and gets new_lens[r] >= 0 more in this
+ * step, or has ended (new_lens[r] = -1).  Its tokens follow those of request r - 1 in the
+ * batch.  free_pages[num_pages] is a ring of page ids: cursor[0] is the place of the
+ * first free one, cursor[1] their number.
+ *   - A request needs ceil((past + new) / page_size) - ceil(past / page_size) pages.
+ *     Requests draw from the ring in order; the first request whose need (with those
+ *     before it) passes the number of free pages is refused, and so is every later one
+ *     that needs any.  A granted request's new page ids go into its block table row.
+ *   - An ended request's pages (those of its past tokens) go to the ring's end, in order
+ *     of request and page; the step itself does not draw them.  Its row stays as it is.
+ * Written: seq_lens[num_seqs] = past + new, or 0 for ended and refused requests (lora_paged_attention
+ * then gives zeros); query_start[num_seqs + 1] = first token of each request; for t <
+ * num_tokens positions[t] = past + index in the request and slots[t] (-1 for refused
+ * requests); tokens past the batch's last get position 0 and slot -1, so a step of fixed size can be
+ * padded.  cursor_out[0..1] = the ring after the step; cursor_out may be cursor (a step
+ * replayed from a graph then advances).  cursor[2] is a scratch word of the call, zero
+ * between calls.  meta[LORA_PLAN_META] = tokens, pages taken, pages given back, requests
+ * refused, invalid entries, free pages after, 0, 0.
+ * Invalid entries: a negative past, new_lens below -1 (the request counts as having no
+ * tokens) or past + new above max_pages * page_size (its tokens get slot -1, its length
+ * 0); a page id outside [0, num_pages) in the ring or in an existing part of a row (the
+ * tokens there get slot -1; it is given back as -1); each token beyond num_tokens (not
+ * written, and query_start stops at num_tokens).
+ * block_table: [num_seqs] rows of max_pages ids, row stride ld_table.  One launch on
+ * `stream` of `device`.  Two calls that share a cursor must not overlap in time.
+ * Errors: INVALID_ARG (a NULL pointer: past_lens, new_lens, seq_lens, block_table may be
+ * NULL with num_seqs = 0, positions and slots with num_tokens = 0, meta always), SHAPE
+ * (num_seqs outside [0, LORA_MAX_SEQS], num_tokens < 0, page_size, num_pages < 1 or too
+ * many, max_pages < 1, ld_table < max_pages, max_pages * page_size above 2^31 - 1).
+ */
+lora_status lora_page_plan(int device, const int32_t* past_lens, const int32_t* new_lens, int num_seqs, int num_tokens,
+                           int page_size, int num_pages, int32_t* free_pages, int32_t* cursor, int32_t* cursor_out,
+                           int32_t* block_table, int ld_table, int max_pages, int32_t* seq_lens, int32_t* query_start,
+                           int32_t* positions, int32_t* slots, int32_t* meta, hipStream_t stream);
+
+/*
+ * Rotary frequencies, radians a position, of rot_dim / 2 pairs: f_i = base^(-2 i /
+ * rot_dim), then scaled for contexts longer than the original_len that the weights were
+ * trained on:
+ *   LORA_ROPE_PLAIN       f_i
+ *   LORA_ROPE_LINEAR      f_i / factor (positions interpolated)
+ *   LORA_ROPE_WAVELENGTH  turns n = original_len f_i / (2 pi): f_i where n >= high, f_i /
+ *                         factor where n <= low, in between w f_i + (1 - w) f_i / factor,
+ *                         w = (n - low) / (high - low)
+ *   LORA_ROPE_DIM         the same blend, linear in the pair's index between the pairs
+ *                         that make `high` and `low` turns over original_len: i_n = rot_dim
+ *                         ln(original_len / (2 pi n)) / (2 ln base), lo = floor(i_high), hi
+ *                         = ceil(i_low), both kept in [0, rot_dim - 1], w = 1 - clamp((i - lo) /
+ *                         max(hi - lo, 0.001), 0, 1)
+ * Pure host function, in double.  Errors: freqs NULL, base <= 1, or (scaled) factor < 1, not finite
+ * -> INVALID_ARG; for the last two original_len <= 0 or not 0 < low < high ->
+ * INVALID_ARG; rot_dim not an even number in [2, LORA_MAX_HEAD_DIM], unknown scaling -> SHAPE.
+ */
+typedef enum { LORA_ROPE_PLAIN = 0, LORA_ROPE_LINEAR = 1, LORA_ROPE_WAVELENGTH = 2, LORA_ROPE_DIM = 3 } lora_rope_scaling;
+lora_status lora_rotary_frequencies(int rot_dim, double base, int scaling, double factor, double original_len, double low,
+                                    double high, double* freqs);
+
+/*
+ * A rotary embedding of the first rot_dim values of a head: pair i turns by position *
+ * freqs[i] and is multiplied by amplitude.  Pairs are (2i, 2i + 1) when `interleaved`, else (i, i
+ * + rot_dim / 2); values past rot_dim pass unchanged.  freqs: host array of rot_dim / 2
+ * values, read during the call (lora_rotary_frequencies, or any others).  Errors: out or
+ * freqs NULL, a frequency or the amplitude not finite -> INVALID_ARG; rot_dim as above -> SHAPE;
+ * NO_DEVICE / OOM.
+ */
+typedef struct lora_rotary lora_rotary;
+lora_status lora_rotary_create(lora_rotary** out, int device, int rot_dim, int interleaved, const double* freqs,
+                               double amplitude);
+lora_status lora_rotary_destroy(lora_rotary* rotary);
+
+/*
+ * Rotary positions on a step's packed q/k/v rows, and the keys and values into the cache:
+ * row t of qkv is [num_q_heads + 2 num_heads][head_dim] (q heads, k heads, v heads; row
+ * stride ldqkv).  q_out[t] (row stride ldq) = the turned q heads, k[slot] = the turned k
+ * heads, v[slot] = the v heads.  Angles are formed in 64 bits, the turn in fp32, one rounding
+ * to the stored type; an e4m3 cache stores x / scale, clamped to [-448, 448], NaN kept.
+ * q_out may be qkv itself (the turn in place; else they must not overlap).  A slot outside
+ * the cache stores nothing; which of two tokens with one slot is kept is not defined.
+ * dtype (of qkv and q_out): LORA_BF16 with a bf16 or e4m3 cache, LORA_F32 with an fp32
+ * one (else DTYPE).  Errors: INVALID_ARG (NULL, or a scale that is not positive and finite), SHAPE (num_tokens < 0,
+ * num_q_heads not a positive multiple of num_heads, rot_dim > head_dim, strides below the rows' width, the cache's
+ * rules), ALIGN (ldqkv, ldq multiples of 8, pointers 16-byte aligned).
+ */
+lora_status lora_rotary_append(const lora_rotary* rotary, const void* qkv, int ldqkv, lora_dtype dtype, int num_q_heads,
+                               const int32_t* positions, const int32_t* slots, int num_tokens, void* q_out, int ldq,
+                               const lora_kv_cache* cache, hipStream_t stream);
+
+/*
+ * Attention of a step's tokens over the paged cache.  The object owns the workspace for
+ * max_seqs sequences and max_tokens new tokens of num_q_heads query and num_kv_heads key/value
+ * heads: partial results of long sequences, which several workgroups share, and the
+ * counters that tell the last of them to join.
+ * Errors of create: out NULL -> INVALID_ARG; max_seqs outside [1, LORA_MAX_SEQS],
+ * max_tokens < 1, num_kv_heads outside [1, 1024], num_q_heads not a multiple of it or
+ * above 1024, head_dim above LORA_MAX_HEAD_DIM -> SHAPE; head_dim not a positive multiple of 16 -> ALIGN;
+ * NO_DEVICE / OOM.
+ */
+typedef struct lora_attention lora_attention;
+lora_status lora_attention_create(lora_attention** out, int device, int max_seqs, int max_tokens, int num_q_heads,
+                                  int num_kv_heads, int head_dim);
+lora_status lora_attention_destroy(lora_attention* attention);
+
+/*
+ * out[t][h] = sum_j softmax_j(scale q[t][h] . k_j) v_j over the cached tokens j that token
+ * t sees: token t is the i-th of the n = query_start[r+1] - query_start[r] new tokens of
+ * its sequence r and stands at position P = seq_lens[r] - n + i; it sees j <= P, and with
+ * window > 0 only j > P - window.  (The new tokens' own keys and values are in the cache:
+ * lora_rotary_append.)  Query head h reads kv head h / (num_q_heads / num_heads).  lse[t][h]
+ * (fp32, may be NULL) = ln sum_j exp(scale q . k_j).  A token that sees nothing (length
+ * 0, absent pages) gets zeros and lse = -inf.  What lies in the cache at unseen places,
+ * infinities and NaN included, has no effect.
+ * q, out: [num_tokens][num_q_heads * head_dim], row strides ldq and ldo, dtype as for
+ * lora_rotary_append (out has q's dtype).  Sums, maxima and products accumulate in fp32,
+ * with one rounding to out.  The result is bitwise the same on every call.  Rows of no sequence are left as
+ * they were; seq_lens outside [0, max_pages * page_size] are taken as the nearer bound,
+ * query_start outside [0, num_tokens] likewise; a sequence that ends before it starts has
+ * no tokens.  One launch on `stream`.  Two calls on one object must not overlap in time.
+ * Errors: INVALID_ARG (NULL pointer, scale not finite, window < 0), SHAPE (heads or
+ * head_dim not the object's, ld_table < max_pages, strides below the rows' width,
+ * max_pages < 1, the cache's rules), CAPACITY (num_seqs or num_tokens above the object's), DTYPE, ALIGN.
+ */
+lora_status lora_paged_attention(const lora_attention* attention, const void* q, int ldq, lora_dtype dtype,
+                                 const lora_kv_cache* cache, const int32_t* block_table, int ld_table, int max_pages,
+                                 const int32_t* seq_lens, const int32_t* query_start, int num_seqs, int num_tokens,
+                                 float scale, int window, void* out, int ldo, float* lse, hipStream_t stream);
+
+/*
  * Index checks (diagnostics): a library built with -DRAXLORA_DEBUG (build.py
  * --debug: libraxlora_debug.so) checks, in its kernels, every index it takes from
  * memory (token ids, slots, sorted positions, workspace rows) against its range; a
@@ -448,13 +614,14 @@ lora_status lora_bandwidth_probe(const void* src, uint64_t read_bytes, void* dst
 
 /*
  * Kernel timing (diagnostics).  While enabled (process-wide), every kernel that
- * the routing, shrink, expand, linear and embedding calls launch is started
+ * the routing, shrink, expand, linear, embedding, page plan, rotary append and paged
+ * attention calls launch is started
  * with hipExtLaunchKernel and a pair of events stamped at that kernel's own start
  * and end, on the stream it runs on.  lora_timing_report waits for the recorded
  * events, writes per kernel id (0 routing, 1 shrink, 2 expand, 3 finish_u: the
  * pass of lora_shrink that adds the k-split partial sums into the caller's u,
- * 4 gather: the embedding rows of lora_embedding; the shrink and expand launches
- * cover both short and long segments) the summed milliseconds and the
+ * 4 gather: the embedding rows of lora_embedding, 5 page_plan, 6 rotary_append, 7
+ * attention; the shrink and expand launches cover both short and long segments) the summed milliseconds and the
  * number of launches into total_ms[0..max_kernels) and launches[0..max_kernels), and
  * clears the record.  lora_timing_kernel_name gives the name of an id ("" if none).
  * Errors: INVALID_ARG for NULL arrays with max_kernels > 0; HIP if an event fails.

@@ -30,8 +30,16 @@ STATUS = {
 }
 globals().update({name: code for code, name in STATUS.items()})
 
+
+class _CKVCache(C.Structure):
+    """lora_kv_cache"""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64), ("token_stride", C.c_int64),
+                ("head_stride", C.c_int64), ("num_pages", C.c_int32), ("page_size", C.c_int32), ("num_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("dtype", C.c_int32), ("k_scale", C.c_float), ("v_scale", C.c_float)]
+
+
 # every symbol declared in include/raxlora.h, with (restype, argtypes)
-_P, _I, _F, _U, _VP = C.c_void_p, C.c_int, C.c_float, C.c_uint, C.c_void_p
+_P, _I, _F, _U, _VP, _D = C.c_void_p, C.c_int, C.c_float, C.c_uint, C.c_void_p, C.c_double
 SIGNATURES = {
     "lora_last_error": (C.c_char_p, []),
     "lora_status_string": (C.c_char_p, [_I]),
@@ -64,12 +72,21 @@ SIGNATURES = {
                                C.POINTER(C.c_int), _I, _VP]),
     "lora_route_linear_group": (_I, [C.POINTER(_P), _I, _P, _VP, _I, C.POINTER(_VP), C.POINTER(C.c_int),
                                      C.POINTER(_VP), C.POINTER(C.c_int), _I, _VP]),
+    "lora_page_plan": (_I, [_I, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "lora_rotary_frequencies": (_I, [_I, _D, _I, _D, _D, _D, _D, C.POINTER(_D)]),
+    "lora_rotary_create": (_I, [C.POINTER(_P), _I, _I, _I, C.POINTER(_D), _D]),
+    "lora_rotary_destroy": (_I, [_P]),
+    "lora_rotary_append": (_I, [_P, _VP, _I, _I, _I, _VP, _VP, _I, _VP, _I, C.POINTER(_CKVCache), _VP]),
+    "lora_attention_create": (_I, [C.POINTER(_P), _I, _I, _I, _I, _I, _I]),
+    "lora_attention_destroy": (_I, [_P]),
+    "lora_paged_attention": (_I, [_P, _VP, _I, _I, C.POINTER(_CKVCache), _VP, _I, _I, _VP, _VP, _I, _I, _F, _I, _VP, _I,
+                                  _VP, _VP]),
     "lora_timing_enable": (_I, [_I]),
     "lora_timing_report": (_I, [C.POINTER(C.c_double), C.POINTER(C.c_int), _I]),
     "lora_timing_kernel_name": (C.c_char_p, [_I]),
 }
 
-KERNEL_NAMES = ["routing", "shrink", "expand", "finish_u", "gather"]
+KERNEL_NAMES = ["routing", "shrink", "expand", "finish_u", "gather", "page_plan", "rotary_append", "attention"]
 
 
 def _load():
@@ -626,3 +643,8 @@ def route_linear_group(pools, routing: Routing, ids, xs, ys, stream=None) -> Non
     _check(lib.lora_route_linear_group(P, n, routing.handle, _ptr(ids) if T else None, T, X, LX, Y, LY, _dt(ys[0]),
                                        _stream(stream) or None), "lora_route_linear_group")
     routing.T = T
+
+
+# the paged-cache operators (page plan, rotary append, paged attention)
+from .kv import *  # noqa: E402,F401,F403
+from . import kv  # noqa: E402,F401

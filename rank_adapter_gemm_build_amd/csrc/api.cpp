@@ -14,8 +14,16 @@
 #include <vector>
 
 #include "common.h"
+#include "host_util.h"
 
 using rax::SlotEntry;
+using rax::aligned16;
+using rax::check_device;
+using rax::DeviceGuard;
+using rax::fail;
+using rax::hip_fail;
+using rax::ok;
+using rax::timer_for;
 
 #ifdef RAXLORA_DEBUG
 namespace rax {   // each kernel translation unit's count of failed index checks
@@ -79,6 +87,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace rax {
+
 lora_status fail(lora_status code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -99,20 +111,6 @@ lora_status hip_fail(hipError_t e, const char* what) {
               hipGetErrorString(e));
 }
 
-// Make `device` current for the scope, restoring the previous device after.
-struct DeviceGuard {
-  int prev = -1;
-  hipError_t err = hipSuccess;
-  explicit DeviceGuard(int device) {
-    err = hipGetDevice(&prev);
-    if (err == hipSuccess && prev != device) err = hipSetDevice(device);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
-
 lora_status check_device(int device) {
   int n = 0;
   hipError_t e = hipGetDeviceCount(&n);
@@ -120,6 +118,10 @@ lora_status check_device(int device) {
   if (device < 0 || device >= n) return fail(LORA_ERR_NO_DEVICE, "device %d out of range [0, %d)", device, n);
   return LORA_OK;
 }
+
+}  // namespace rax
+
+namespace {
 
 // ------------------------------------------------------------- kernel timing
 // When enabled, each hot-path launch takes a pair of events that hipExtLaunchKernel
@@ -144,20 +146,25 @@ hipEvent_t take_event() {
   return e;
 }
 
-rax::KTimer timer_for(int kernel) {
-  rax::KTimer t;
+}  // namespace
+
+namespace rax {
+KTimer timer_for(int kernel) {
+  KTimer t;
   std::lock_guard<std::mutex> lk(g_timing_mu);
   if (!g_timing_on) return t;
   t.start = take_event();
   t.stop = take_event();
-  if (!t.start || !t.stop) return rax::KTimer{};
+  if (!t.start || !t.stop) return KTimer{};
   g_timing_records.push_back(TimingRecord{kernel, t.start, t.stop});
   return t;
 }
+}  // namespace rax
 
-const char* const kKernelNames[rax::kKernelCount] = {"routing", "shrink", "expand", "finish_u", "gather"};
+namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+const char* const kKernelNames[rax::kKernelCount] = {"routing",  "shrink",    "expand",        "finish_u",
+                                                      "gather",   "page_plan", "rotary_append", "attention"};
 
 int env_int(const char* name, int dflt) {
   const char* v = getenv(name);

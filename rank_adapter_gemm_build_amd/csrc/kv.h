@@ -1,0 +1,49 @@
+// Launchers of the operators between the packed q/k/v projection and the o projection:
+// page plan, rotary append, paged attention (device code in the .hip files).
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include "common.h"
+#include "kv_index.h"
+
+namespace rax {
+
+struct PagePlanArgs {
+  const int32_t *past, *fresh;
+  int32_t *ring, *cursor, *cursor_out, *table, *seq_lens, *query_start, *positions, *slots, *meta;
+  int num_seqs, num_tokens, page_shift, num_pages, ld_table, max_pages;
+};
+hipError_t launch_page_plan(const PagePlanArgs& a, hipStream_t stream, const KTimer& tm);
+
+// A layer's cache as the kernels address it (strides in elements)
+struct CacheView {
+  void *k, *v;
+  long long page_stride, token_stride, head_stride;
+  int num_pages, page_shift, heads, dim, dtype;
+  float k_scale, v_scale;
+};
+
+struct RotaryArgs {
+  const void* qkv;
+  void* q_out;
+  const int32_t *positions, *slots;
+  const double* turns;   // [rot / 2]: turns a position
+  CacheView c;
+  int ldqkv, ldq, dtype, q_heads, num_tokens, rot, interleaved;
+  float amplitude;
+};
+hipError_t launch_rotary_append(const RotaryArgs& a, hipStream_t stream, const KTimer& tm);
+
+struct AttentionArgs {
+  const void* q;
+  void* out;
+  float* lse;            // may be null
+  const int32_t *table, *seq_lens, *query_start;
+  CacheView c;
+  int ldq, ldo, dtype, q_heads, num_seqs, num_tokens, ld_table, max_pages, window;
+  float scale;
+};
+hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t stream, const KTimer& tm);
+
+}  // namespace rax
