@@ -554,8 +554,9 @@ lora_status lora_rotary_append(const lora_rotary* rotary, const void* qkv, int l
  * heads: partial results of long sequences, which several workgroups share, and the
  * counters that tell the last of them to join.
  * Errors of create: out NULL -> INVALID_ARG; max_seqs outside [1, LORA_MAX_SEQS],
- * max_tokens < 1, num_kv_heads outside [1, 1024], num_q_heads not a multiple of it or
- * above 1024, head_dim above LORA_MAX_HEAD_DIM -> SHAPE; head_dim not a positive multiple of 16 -> ALIGN;
+ * max_tokens outside [1, 2^24] or, times num_q_heads / num_kv_heads, above 2^30, num_kv_heads outside
+ * [1, 1024], num_q_heads not a multiple of it or above 1024, head_dim above
+ * LORA_MAX_HEAD_DIM -> SHAPE; head_dim not a positive multiple of 16 -> ALIGN;
  * NO_DEVICE / OOM.
  */
 typedef struct lora_attention lora_attention;

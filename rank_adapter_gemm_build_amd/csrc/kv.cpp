@@ -27,7 +27,22 @@ struct lora_rotary {
 
 struct lora_attention {
   int device = 0, max_seqs = 0, max_tokens = 0, q_heads = 0, kv_heads = 0, dim = 0;
+  int workers = 0, part_rows = 0;
+  float *part_o = nullptr, *part_ml = nullptr;   // device
+  int* arrived = nullptr;                        // device, zero between calls
 };
+
+namespace rax {
+// Rows (new tokens times query heads of a kv head) that a workgroup takes of a sequence:
+// as many of its waves share rows as the mean sequence of the batch fills; the other waves
+// split the keys.
+AttnRows attention_rows(long long rows) {
+  if (rows <= 16) return {1, 1};
+  if (rows <= 32) return {2, 1};
+  if (rows <= 64) return {2, 2};
+  return {2, 4};
+}
+}  // namespace rax
 
 namespace {
 
@@ -290,22 +305,48 @@ lora_status lora_attention_create(lora_attention** out, int device, int max_seqs
   if (num_kv_heads < 1 || num_kv_heads > 1024 || num_q_heads < 1 || num_q_heads > 1024 || num_q_heads % num_kv_heads)
     return fail(LORA_ERR_SHAPE, "num_q_heads %d must be a multiple of num_kv_heads %d, both in [1, 1024]", num_q_heads,
                 num_kv_heads);
+  if ((long long)max_tokens * (num_q_heads / num_kv_heads) > (1LL << 30))
+    return fail(LORA_ERR_SHAPE, "max_tokens %d times %d query heads of a kv head is above 2^30", max_tokens,
+                num_q_heads / num_kv_heads);
   lora_status st = check_head_dim(head_dim);
   if (st != LORA_OK) return st;
   if ((st = check_device(device)) != LORA_OK) return st;
+  DeviceGuard g(device);
+  if (g.err != hipSuccess) return hip_fail(g.err, "hipSetDevice");
+  int cus = 0;
+  hipError_t e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+  if (e != hipSuccess) return hip_fail(e, "hipDeviceGetAttribute");
   lora_attention* a = new (std::nothrow) lora_attention;
   if (!a) return fail(LORA_ERR_OOM, "out of host memory");
   a->device = device;
+  // two workgroups a compute unit fit in registers and LDS
+  a->workers = std::min(rax::kMaxParts, std::max(8, 2 * cus / 8 * 8));
+  a->part_rows = rax::attention_rows((long long)max_tokens * (num_q_heads / num_kv_heads)).rows();
   a->max_seqs = max_seqs;
   a->max_tokens = max_tokens;
   a->q_heads = num_q_heads;
   a->kv_heads = num_kv_heads;
   a->dim = head_dim;
+  const size_t part = 2 * (size_t)a->workers * a->part_rows * sizeof(float);
+  e = hipMalloc(reinterpret_cast<void**>(&a->part_o), part * head_dim);
+  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->part_ml), part * 2);
+  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->arrived), a->workers * sizeof(int));
+  if (e == hipSuccess) e = hipMemset(a->arrived, 0, a->workers * sizeof(int));
+  if (e == hipSuccess) e = hipDeviceSynchronize();
+  if (e != hipSuccess) {
+    (void)lora_attention_destroy(a);
+    return hip_fail(e, "attention workspace");
+  }
   *out = a;
   return ok();
 }
 
 lora_status lora_attention_destroy(lora_attention* attention) {
+  if (!attention) return ok();
+  DeviceGuard g(attention->device);
+  if (attention->part_o) (void)hipFree(attention->part_o);
+  if (attention->part_ml) (void)hipFree(attention->part_ml);
+  if (attention->arrived) (void)hipFree(attention->arrived);
   delete attention;
   return ok();
 }
@@ -357,6 +398,16 @@ lora_status lora_paged_attention(const lora_attention* attention, const void* q,
   a.max_pages = max_pages;
   a.window = window;
   a.scale = scale;
+  const rax::AttnRows rows =
+      rax::attention_rows(((long long)num_tokens + num_seqs - 1) / num_seqs * (attention->q_heads / attention->kv_heads));
+  a.row_tiles = rows.tiles;
+  a.row_waves = rows.waves;
+  a.workers = attention->workers;
+  a.min_steps = 2;
+  a.part_rows = attention->part_rows;
+  a.part_o = attention->part_o;
+  a.part_ml = attention->part_ml;
+  a.arrived = attention->arrived;
   const hipError_t e = rax::launch_paged_attention(a, stream, timer_for(rax::kKAttention));
   if (e != hipSuccess) return hip_fail(e, "paged attention launch");
   return ok();

@@ -43,7 +43,20 @@ struct AttentionArgs {
   CacheView c;
   int ldq, ldo, dtype, q_heads, num_seqs, num_tokens, ld_table, max_pages, window;
   float scale;
+  // the launch's shape and workspace
+  int row_tiles, row_waves;   // rows of a workgroup: 16 * row_tiles * row_waves
+  int workers, min_steps;     // workgroups; steps each has at least
+  int part_rows;              // rows of a slot of part_o and part_ml
+  float *part_o, *part_ml;    // two slots a workgroup: [part_rows][dim], [part_rows][2]
+  int* arrived;               // a counter a workgroup, zero between launches
 };
+// workgroups a launch has at most (the join keeps a weight of each in LDS), a multiple of 8
+constexpr int kMaxParts = 512;
+struct AttnRows {
+  int tiles, waves;
+  int rows() const { return 16 * tiles * waves; }
+};
+AttnRows attention_rows(long long rows);
 hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t stream, const KTimer& tm);
 
 }  // namespace rax

@@ -94,4 +94,33 @@ RAX_HD KeyRange token_keys(int i, int n, int len, int window) {
   return k;
 }
 
+// What a sequence is to the attention's workgroups: its keys (those any of its new tokens
+// sees), from `base`, a multiple of 16, in `steps` runs of step_keys; at least one step
+// where there are new tokens, so that rows which see nothing are written too.
+struct SeqSpan {
+  unsigned base;
+  int steps;
+};
+RAX_HD SeqSpan seq_span(const SeqRows& s, int window, int step_keys) {
+  SeqSpan x{0u, 0};
+  if (s.n <= 0) return x;
+  const KeyRange first = token_keys(0, s.n, s.len, window), last = token_keys(s.n - 1, s.n, s.len, window);
+  x.base = (unsigned)first.lo & ~15u;
+  const unsigned hi = (unsigned)last.hi, span = hi > x.base ? hi - x.base : 0u;
+  x.steps = (int)((span + (unsigned)step_keys - 1u) / (unsigned)step_keys);
+  if (x.steps < 1) x.steps = 1;
+  return x;
+}
+
+// Contiguous equal shares of `work` steps: worker b of g takes [share_start(b), share_start(b + 1)).
+RAX_HD long long share_start(long long work, int g, int b) {
+  const long long q = work / g, rem = work - q * g;
+  return q * b + (b < rem ? b : rem);
+}
+// the worker whose share holds step x (0 <= x < work)
+RAX_HD int share_owner(long long work, int g, long long x) {
+  const long long q = work / g, rem = work - q * g, wide = rem * (q + 1);
+  return (int)(x < wide ? x / (q + 1) : rem + (x - wide) / q);
+}
+
 }  // namespace rax

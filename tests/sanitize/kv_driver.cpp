@@ -18,6 +18,11 @@ hipError_t launch_rotary_append(const RotaryArgs&, hipStream_t, const KTimer&) {
 hipError_t launch_paged_attention(const AttentionArgs&, hipStream_t, const KTimer&) { ++g_launches; return hipSuccess; }
 }  // namespace rax
 
+extern "C" hipError_t hipDeviceGetAttribute(int* v, hipDeviceAttribute_t, int) {
+  *v = 8;
+  return hipSuccess;
+}
+
 static int failures = 0;
 #define EXPECT(call, want)                                                                                \
   do {                                                                                                    \
@@ -105,6 +110,7 @@ static void cache_refusals() {
   EXPECT(lora_attention_create(&a, 0, 0, 8, 4, 2, 32), LORA_ERR_SHAPE);
   EXPECT(lora_attention_create(&a, 0, LORA_MAX_SEQS + 1, 8, 4, 2, 32), LORA_ERR_SHAPE);
   EXPECT(lora_attention_create(&a, 0, 4, 0, 4, 2, 32), LORA_ERR_SHAPE);
+  EXPECT(lora_attention_create(&a, 0, 4, 1 << 24, 1024, 1, 32), LORA_ERR_SHAPE);
   EXPECT(lora_attention_create(&a, 0, 4, 8, 5, 2, 32), LORA_ERR_SHAPE);
   EXPECT(lora_attention_create(&a, 0, 4, 8, 4, 0, 32), LORA_ERR_SHAPE);
   EXPECT(lora_attention_create(&a, 0, 4, 8, 2048, 2, 32), LORA_ERR_SHAPE);
@@ -268,7 +274,40 @@ static void index_walk() {
   }
 }
 
+// the attention's line of steps: equal contiguous shares that cover it once, and the spans
+// of the sequences that make it up
+static void share_walk() {
+  std::mt19937 g(11);
+  for (int i = 0; i < 3000; ++i) {
+    const long long work = 1 + (i % 3 ? g() % 500 : (long long)g() << (g() % 20));
+    const int n = 1 + (int)(g() % std::min<long long>(work, 512));
+    TRUE(rax::share_start(work, n, 0) == 0 && rax::share_start(work, n, n) == work);
+    for (int b = 0; b < n; ++b) {
+      const long long x0 = rax::share_start(work, n, b), x1 = rax::share_start(work, n, b + 1);
+      TRUE(x1 > x0 && x1 - x0 <= work / n + 1);
+      TRUE(rax::share_owner(work, n, x0) == b && rax::share_owner(work, n, x1 - 1) == b);
+    }
+  }
+  for (int i = 0; i < 20000; ++i) {
+    const int max_len = i % 2 ? 16 * (1 + (int)(g() % 40)) : INT_MAX / 16 * 16, T = 1 + (int)(g() % 50);
+    const rax::SeqRows s = rax::seq_rows((int)(g() % 60), (int)(g() % 60), (int)(g() % 3 ? g() % 700 : g()), T, max_len);
+    const int window = g() % 2 ? 0 : (int)(g() % 3 ? g() % 300 : g() >> 1), step = 16 << (g() % 4);
+    const rax::SeqSpan x = rax::seq_span(s, window, step);
+    TRUE((x.steps == 0) == (s.n == 0) && x.base % 16 == 0);
+    for (int t = 0; t < s.n; ++t) {
+      const rax::KeyRange k = rax::token_keys(t, s.n, s.len, window);
+      if (k.hi > k.lo) TRUE((unsigned)k.lo >= x.base && (unsigned)k.hi <= x.base + (unsigned long long)x.steps * step);
+    }
+    if (x.steps > 1) TRUE(x.base + (unsigned long long)(x.steps - 1) * step < (unsigned)s.len);
+  }
+  for (long long rows : {1LL, 16LL, 17LL, 33LL, 65LL, 1LL << 30}) {
+    const rax::AttnRows r = rax::attention_rows(rows);
+    TRUE(4 % r.waves == 0 && (rows > 128 || r.rows() >= rows) && r.rows() <= 128);
+  }
+}
+
 int main() {
+  share_walk();
   plan_refusals();
   cache_refusals();
   frequency_refusals();
