@@ -52,10 +52,6 @@ constexpr int kAttnWaves = kAttnThreads / 64;
 typedef const __attribute__((address_space(4))) int32_t* const_words_t;
 __device__ __forceinline__ const_words_t const_words(const int32_t* p) { return (const_words_t)(uintptr_t)p; }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ long long uniform(long long v) {
-  const unsigned lo = (unsigned)uniform((int)v), hi = (unsigned)uniform((int)(v >> 32));
-  return (long long)(((unsigned long long)hi << 32) | lo);
-}
 
 // Cells are read through buffer descriptors, whose base is a group of keys at one kv head:
 // the lane's part of an address is one register, kept for all tiles, and a lane whose
@@ -83,6 +79,26 @@ template <int N> __device__ __forceinline__ Words<N> load_words(__amdgpu_buffer_
   }
   return x;
 }
+
+// What workgroups hand to each other inside a launch goes past the caches that the XCDs do
+// not share (agent scope, bit sc1), access by access; a fence of that scope would write back
+// and drop the whole L2 instead, which took some 10 us each time.
+constexpr int kAgentScope = 16;
+__device__ __forceinline__ void put_shared(__amdgpu_buffer_rsrc_t r, uint32_t ofs, f32x4_t v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, ofs, 0, kAgentScope);
+}
+__device__ __forceinline__ f32x4_t get_shared(__amdgpu_buffer_rsrc_t r, uint32_t ofs) {
+  return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, ofs, 0, kAgentScope));
+}
+__device__ __forceinline__ void put_shared2(__amdgpu_buffer_rsrc_t r, uint32_t ofs, float x, float y) {
+  __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(x), __float_as_uint(y)}, r, ofs, 0, kAgentScope);
+}
+__device__ __forceinline__ float2 get_shared2(__amdgpu_buffer_rsrc_t r, uint32_t ofs) {
+  const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(r, ofs, 0, kAgentScope);
+  return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+}
+// every store of this wave has arrived
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // maximum and sum over the four lanes that share lane % 16
 __device__ __forceinline__ float max_over_groups(float v) {
@@ -136,35 +152,39 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
   constexpr int G = S::kGroups, NK = S::kKLoads, NQ = S::kQFrags, EC = S::kEC, VB = S::kVB, VW = S::kVW;
   __shared__ float buf[kAttnWaves][16][S::kPitch];
   __shared__ float ml[kAttnWaves][RT][16][2];
-  __shared__ long long part_s[kAttnWaves], start_s;
-  __shared__ int seq_s, last_s;
+  __shared__ int part_s[kAttnWaves], start_s, seq_s, last_s;
   static_assert(sizeof(buf) >= 8 * kMaxParts * sizeof(float), "the join's weights lie in buf");
 
   const int tid = threadIdx.x, lane = lane_id(), w = uniform(tid >> 6);
   const int c16 = lane & 15, g4 = lane >> 4;
-  const int D = a.c.dim, ps = a.c.page_shift, max_len = a.max_pages << ps, group = a.q_heads / a.c.heads;
-  const int row_waves = a.row_waves, key_waves = kAttnWaves / row_waves, rw = w % row_waves, kw = w / row_waves;
-  const int rows_wg = 16 * RT * row_waves, step_keys = key_waves * S::kKeys;
+  const int D = a.c.dim, ps = a.c.page_shift, max_len = a.max_pages << ps, group = a.group_size;
+  const int rw_log2 = a.row_waves >> 1, row_waves = a.row_waves, kw_log2 = 2 - rw_log2, key_waves = 1 << kw_log2;   // 1, 2 or 4
+  const int rw = w & (row_waves - 1), kw = w >> rw_log2;
+  constexpr int kRowsLog2 = RT == 2 ? 5 : 4, kKeysLog2 = S::kF32 ? 4 : 5;
+  const int rows_log2 = kRowsLog2 + rw_log2, rows_wg = 1 << rows_log2;
+  const int tiles_log2 = a.step_log2 - kKeysLog2;   // tiles of a step
   const const_words_t lens = const_words(a.seq_lens), starts = const_words(a.query_start);
 
   // ---- this workgroup's share: the line's length, then the sequence that its first step falls in
-  auto units_of = [&](const SeqRows& s) { return (long long)a.c.heads * ((s.n * (long long)group + rows_wg - 1) / rows_wg); };
+  auto steps_of = [&](const SeqRows& s) {
+    return a.c.heads * row_blocks(s.n, group, rows_log2) * seq_span(s, a.window, a.step_log2).steps;
+  };
   const int per = (a.num_seqs + kAttnThreads - 1) / kAttnThreads;
   const int r0 = min(a.num_seqs, tid * per), r1 = min(a.num_seqs, r0 + per);
-  long long mine = 0;
+  int mine = 0;
   for (int r = r0; r < r1; ++r) {
     const SeqRows s = seq_rows(a.query_start[r], a.query_start[r + 1], a.seq_lens[r], a.num_tokens, max_len);
-    mine += units_of(s) * seq_span(s, a.window, step_keys).steps;
+    mine += steps_of(s);
   }
-  long long scan = mine;
+  int scan = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const long long y = __shfl_up(scan, d);
+    const int y = __shfl_up(scan, d);
     if (lane >= d) scan += y;
   }
   if (lane == 63) part_s[w] = scan;
   __syncthreads();
-  long long work = 0, before = scan - mine;
+  int work = 0, before = scan - mine;
 #pragma unroll
   for (int v = 0; v < kAttnWaves; ++v) {
     if (v < w) before += part_s[v];
@@ -172,17 +192,17 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
   }
   work = uniform(work);
   if (work == 0) return;
-  const long long full = (work + a.min_steps - 1) / a.min_steps;
+  const int full = (work + a.min_steps - 1) / a.min_steps;
   const int workers = full < (long long)gridDim.x ? (int)full : (int)gridDim.x;
   // neighbouring shares on one XCD: the row blocks of a head read its keys from one L2
   const int b = (int)(blockIdx.x % kXcds) * (int)(gridDim.x / kXcds) + (int)(blockIdx.x / kXcds);
   if (b >= workers) return;
-  const long long x0 = share_start(work, workers, b), x1 = share_start(work, workers, b + 1);
+  const int x0 = share_start(work, workers, b), x1 = share_start(work, workers, b + 1);
   if (mine > 0 && x0 >= before && x0 < before + mine) {
-    long long at = before;
+    int at = before;
     for (int r = r0; r < r1; ++r) {
       const SeqRows s = seq_rows(a.query_start[r], a.query_start[r + 1], a.seq_lens[r], a.num_tokens, max_len);
-      const long long n = units_of(s) * seq_span(s, a.window, step_keys).steps;
+      const int n = steps_of(s);
       if (x0 < at + n) {
         seq_s = r;
         start_s = at;
@@ -193,7 +213,7 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
   }
   __syncthreads();
   int r = uniform(seq_s);
-  long long seq_at = uniform(start_s);
+  int seq_at = uniform(start_s);
 
   const uint32_t tok_b = (uint32_t)a.c.token_stride * (uint32_t)sizeof(C);   // below 2^27
   const float qs = a.scale * a.c.k_scale * 1.44269504088896341f;
@@ -207,19 +227,18 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
     vofs[vb] = d < D ? (uint32_t)(4 * g4) * tok_b + d * (uint32_t)sizeof(C) : kNowhere;
   }
 
-  for (long long x = x0; x < x1;) {
+  for (int x = x0; x < x1;) {
     const SeqRows s = seq_rows(starts[r], starts[r + 1], lens[r], a.num_tokens, max_len);
-    const SeqSpan span = seq_span(s, a.window, step_keys);
-    const int blocks = (int)((s.n * (long long)group + rows_wg - 1) / rows_wg);
-    const long long seq_work = (long long)a.c.heads * blocks * span.steps;
+    const SeqSpan span = seq_span(s, a.window, a.step_log2);
+    const int blocks = row_blocks(s.n, group, rows_log2), seq_work = a.c.heads * blocks * span.steps;
     if (x >= seq_at + seq_work) {
       seq_at += seq_work;
       ++r;
       continue;
     }
-    const long long unit = (x - seq_at) / span.steps, unit_at = seq_at + unit * span.steps;
-    const int s0 = (int)(x - unit_at), s1 = (int)min((long long)span.steps, x1 - unit_at);
-    const int kh = (int)(unit / blocks), row0 = (int)(unit - (long long)kh * blocks) * rows_wg;
+    const int unit = (int)((unsigned)(x - seq_at) / (unsigned)span.steps), unit_at = seq_at + unit * span.steps;
+    const int s0 = x - unit_at, s1 = min(span.steps, x1 - unit_at);
+    const int kh = blocks == 1 ? unit : (int)((unsigned)unit / (unsigned)blocks), row0 = (unit - kh * blocks) * rows_wg;
     const int rows = min(rows_wg, s.n * group - row0);
     x = unit_at + s1;
 
@@ -231,7 +250,7 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
     for (int rt = 0; rt < RT; ++rt) {
       const int row = wrow0 + rt * 16 + c16;
       const bool there = rt * 16 + c16 < wrows;
-      const int i = there ? row / group : 0, h = there ? kh * group + row - i * group : 0;
+      const int i = there ? fast_quot(row, a.group) : 0, h = there ? kh * group + row - i * group : 0;
       const KeyRange k = token_keys(i, s.n, s.len, a.window);
       lo[rt] = there ? k.lo : 0;
       hi[rt] = there ? k.hi : 0;
@@ -258,19 +277,19 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
     // ---- tiles of this wave: those of the share that any (all) of its rows see
     unsigned any_lo = 0, any_hi = 0, all_lo = 0, all_hi = 0;
     if (wrows > 0) {
-      const KeyRange k0 = token_keys(wrow0 / group, s.n, s.len, a.window);
-      const KeyRange k1 = token_keys((wrow0 + wrows - 1) / group, s.n, s.len, a.window);
+      const KeyRange k0 = token_keys(fast_quot(wrow0, a.group), s.n, s.len, a.window);
+      const KeyRange k1 = token_keys(fast_quot(wrow0 + wrows - 1, a.group), s.n, s.len, a.window);
       any_lo = k0.lo;
       any_hi = k1.hi;
       all_lo = k1.lo;
       all_hi = k0.hi;
     }
-    const unsigned tile_end = (unsigned)s1 * key_waves;
-    unsigned t = (unsigned)s0 * key_waves + kw, t_end = t;
+    const unsigned tile_end = (unsigned)s1 << tiles_log2;
+    unsigned t = ((unsigned)s0 << tiles_log2) + kw, t_end = t;
     if (any_hi > any_lo) {
       t_end = min(tile_end, (any_hi - span.base + S::kKeys - 1) / S::kKeys);
       const unsigned first = any_lo > span.base ? (any_lo - span.base) / S::kKeys : 0u;
-      if (first > t) t += (first - t + key_waves - 1) / key_waves * key_waves;
+      if (first > t) t += (first - t + key_waves - 1) >> kw_log2 << kw_log2;
     }
     t = (unsigned)uniform((int)t);
     t_end = (unsigned)uniform((int)t_end);
@@ -519,8 +538,9 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
     const bool whole = s0 == 0 && s1 == span.steps;
     const int first_wg = whole ? b : share_owner(work, workers, unit_at);
     const int slot = s0 == 0 ? 2 * b + 1 : 2 * b;
-    float* part_o = a.part_o + (size_t)slot * a.part_rows * D;
-    float* part_ml = a.part_ml + (size_t)slot * a.part_rows * 2;
+    const uint32_t slot_row = (uint32_t)slot * a.part_rows;   // the workspace stays below 2^31 bytes
+    const auto part_o = cells_at(reinterpret_cast<const char*>(a.part_o), true);
+    const auto part_ml = cells_at(reinterpret_cast<const char*>(a.part_ml), true);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       l[rt] = sum_over_groups(l[rt]);
@@ -561,30 +581,26 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
             acc += *reinterpret_cast<const f32x4_t*>(&buf[v][row16][d4 * 4]);
           }
           if (whole) {
-            const int row = row0 + lrow, i = row / group, h = kh * group + row - i * group;
+            const int row = row0 + lrow, i = fast_quot(row, a.group), h = kh * group + row - i * group;
             write_row<T>(a, s.start + i, h, d, acc, mm, ll);
           } else {
-            *reinterpret_cast<f32x4_t*>(part_o + (size_t)lrow * D + d) = acc;
-            if (d == 0) {
-              part_ml[2 * lrow] = mm;
-              part_ml[2 * lrow + 1] = ll;
-            }
+            put_shared(part_o, ((slot_row + lrow) * D + d) * 4, acc);
+            if (d == 0) put_shared2(part_ml, (slot_row + lrow) * 8, mm, ll);
           }
         }
       }
     }
     if (!whole) {
       const int last_wg = share_owner(work, workers, unit_at + span.steps - 1), parts = last_wg - first_wg + 1;
-      __threadfence();
+      stores_done();
       __syncthreads();
       if (tid == 0) {
-        const int n = atomicAdd(&a.arrived[first_wg], 1);
+        const int n = __hip_atomic_fetch_add(&a.arrived[first_wg], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         last_s = n == parts - 1;
-        if (last_s) a.arrived[first_wg] = 0;
+        if (last_s) __hip_atomic_store(&a.arrived[first_wg], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
       __syncthreads();
       if (last_s) {
-        __threadfence();
         float* weight = &buf[0][0][0];   // [8][parts]
         for (int y0 = 0; y0 < rows; y0 += 8) {
           {   // 32 threads a row: maximum, sum, weights of the parts
@@ -592,16 +608,16 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
             float mm = -INFINITY, ll = 0.f;
             if (lrow < rows) {
               for (int p = i0; p < parts; p += 32)
-                mm = fmaxf(mm, a.part_ml[((size_t)part_slot(first_wg, p) * a.part_rows + lrow) * 2]);
+                mm = fmaxf(mm, get_shared2(part_ml, ((uint32_t)part_slot(first_wg, p) * a.part_rows + lrow) * 8).x);
             }
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
             if (lrow < rows) {
               for (int p = i0; p < parts; p += 32) {
-                const float* x2 = a.part_ml + ((size_t)part_slot(first_wg, p) * a.part_rows + lrow) * 2;
-                const float f = x2[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x2[0] - mm);
+                const float2 x2 = get_shared2(part_ml, ((uint32_t)part_slot(first_wg, p) * a.part_rows + lrow) * 8);
+                const float f = x2.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x2.x - mm);
                 weight[y * kMaxParts + p] = f;
-                ll += x2[1] * f;
+                ll += x2.y * f;
               }
             }
 #pragma unroll
@@ -612,16 +628,20 @@ __global__ __launch_bounds__(kAttnThreads, DB > 128 ? 1 : 2) void paged_attentio
             }
           }
           __syncthreads();
-          const int chunks = D / 4;
-          for (int it = tid; it < 8 * chunks; it += kAttnThreads) {
-            const int y = it / chunks, d = (it - y * chunks) * 4, lrow = y0 + y;
-            if (lrow >= rows) continue;
+          for (int it = tid; it < 8 * DB / 4; it += kAttnThreads) {
+            const int y = it / (DB / 4), d = it % (DB / 4) * 4, lrow = y0 + y;
+            if (lrow >= rows || d >= D) continue;
             f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-            for (int p = 0; p < parts; ++p)
-              acc += weight[y * kMaxParts + p] *
-                     *reinterpret_cast<const f32x4_t*>(a.part_o + ((size_t)part_slot(first_wg, p) * a.part_rows + lrow) * D + d);
-            const int row = row0 + lrow, i = row / group, h = kh * group + row - i * group;
+            for (int p0 = 0; p0 < parts; p0 += 8) {
+              f32x4_t v[8];
+#pragma unroll
+              for (int p = 0; p < 8; ++p)
+                v[p] = get_shared(part_o, p0 + p < parts ? (((uint32_t)part_slot(first_wg, p0 + p) * a.part_rows + lrow) * D + d) * 4 : kNowhere);
+#pragma unroll
+              for (int p = 0; p < 8; ++p)
+                if (p0 + p < parts) acc += weight[y * kMaxParts + p0 + p] * v[p];
+            }
+            const int row = row0 + lrow, i = fast_quot(row, a.group), h = kh * group + row - i * group;
             write_row<T>(a, s.start + i, h, d, acc, ml[0][0][y][0], ml[0][0][y][1]);
           }
           __syncthreads();

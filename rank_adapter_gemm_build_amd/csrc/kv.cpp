@@ -404,6 +404,10 @@ lora_status lora_paged_attention(const lora_attention* attention, const void* q,
   a.row_waves = rows.waves;
   a.workers = attention->workers;
   a.min_steps = 2;
+  a.group_size = attention->q_heads / attention->kv_heads;
+  a.group = rax::fast_div(a.group_size);
+  a.step_log2 = rax::line_step_log2(rax::attention_step_log2(a), num_seqs, num_tokens, max_pages * cache->page_size,
+                                    attention->kv_heads, a.group_size, log2_of(rows.rows()));
   a.part_rows = attention->part_rows;
   a.part_o = attention->part_o;
   a.part_ml = attention->part_ml;

@@ -46,6 +46,9 @@ struct AttentionArgs {
   // the launch's shape and workspace
   int row_tiles, row_waves;   // rows of a workgroup: 16 * row_tiles * row_waves
   int workers, min_steps;     // workgroups; steps each has at least
+  int step_log2;              // keys of a step
+  int group_size;             // query heads of a kv head
+  FastDiv group;
   int part_rows;              // rows of a slot of part_o and part_ml
   float *part_o, *part_ml;    // two slots a workgroup: [part_rows][dim], [part_rows][2]
   int* arrived;               // a counter a workgroup, zero between launches
@@ -57,6 +60,13 @@ struct AttnRows {
   int rows() const { return 16 * tiles * waves; }
 };
 AttnRows attention_rows(long long rows);
+// keys that a workgroup's waves take at a time (log2): 16 (fp32) or 32 each, the waves that
+// do not share rows side by side
+inline int attention_step_log2(const AttentionArgs& a) {
+  int s = a.dtype == LORA_F32 ? 6 : 7;
+  for (int w = a.row_waves; w > 1; w /= 2) --s;
+  return s;
+}
 hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t stream, const KTimer& tm);
 
 }  // namespace rax

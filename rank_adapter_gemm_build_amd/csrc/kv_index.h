@@ -101,26 +101,57 @@ struct SeqSpan {
   unsigned base;
   int steps;
 };
-RAX_HD SeqSpan seq_span(const SeqRows& s, int window, int step_keys) {
+RAX_HD SeqSpan seq_span(const SeqRows& s, int window, int step_log2) {
   SeqSpan x{0u, 0};
   if (s.n <= 0) return x;
   const KeyRange first = token_keys(0, s.n, s.len, window), last = token_keys(s.n - 1, s.n, s.len, window);
   x.base = (unsigned)first.lo & ~15u;
   const unsigned hi = (unsigned)last.hi, span = hi > x.base ? hi - x.base : 0u;
-  x.steps = (int)((span + (unsigned)step_keys - 1u) / (unsigned)step_keys);
+  x.steps = (int)((span + ((1u << step_log2) - 1u)) >> step_log2);
   if (x.steps < 1) x.steps = 1;
   return x;
 }
+// Units of a sequence: kv heads times blocks of 2^rows_log2 rows.
+RAX_HD int row_blocks(int n, int group, int rows_log2) {
+  return (int)(((unsigned)n * (unsigned)group + ((1u << rows_log2) - 1u)) >> rows_log2);   // n * group <= 2^30
+}
+// The least step_log2 >= least with which the line of all units' steps is below 2^31
+// whatever the lengths on the device are (no more than max_len keys and num_tokens tokens
+// a sequence).
+RAX_HD int line_step_log2(int least, int num_seqs, int num_tokens, int max_len, int heads, int group, int rows_log2) {
+  const double units = (double)num_seqs * heads * row_blocks(num_tokens, group, rows_log2);
+  int s = least;
+  while (s < 31 && units * ((double)(max_len >> s) + 2.0) >= 2147483648.0) ++s;
+  return s;
+}
 
 // Contiguous equal shares of `work` steps: worker b of g takes [share_start(b), share_start(b + 1)).
-RAX_HD long long share_start(long long work, int g, int b) {
-  const long long q = work / g, rem = work - q * g;
-  return q * b + (b < rem ? b : rem);
+RAX_HD int share_start(int work, int g, int b) {
+  const unsigned q = (unsigned)work / (unsigned)g, rem = (unsigned)work - q * (unsigned)g;
+  return (int)(q * (unsigned)b + ((unsigned)b < rem ? (unsigned)b : rem));
 }
 // the worker whose share holds step x (0 <= x < work)
-RAX_HD int share_owner(long long work, int g, long long x) {
-  const long long q = work / g, rem = work - q * g, wide = rem * (q + 1);
-  return (int)(x < wide ? x / (q + 1) : rem + (x - wide) / q);
+RAX_HD int share_owner(int work, int g, int x) {
+  const unsigned q = (unsigned)work / (unsigned)g, rem = (unsigned)work - q * (unsigned)g, wide = rem * (q + 1u);
+  return (int)((unsigned)x < wide ? (unsigned)x / (q + 1u) : rem + ((unsigned)x - wide) / q);
+}
+
+// Division by a fixed d in [1, 1024] of numbers below 2^31: with s = floor(log2 d), n / d =
+// (n ceil(2^(32 + s) / d)) >> (32 + s), as the multiplier's excess, below d < 2^(s + 1),
+// times n stays below 2^(32 + s); a power of two is the shift alone (mul 0).
+struct FastDiv {
+  unsigned mul;
+  int shift;
+};
+inline FastDiv fast_div(int d) {
+  FastDiv f{0u, 0};
+  while ((2 << f.shift) <= d) ++f.shift;
+  if (d != 1 << f.shift) f.mul = (unsigned)(((1ULL << (32 + f.shift)) + (unsigned)d - 1u) / (unsigned)d);
+  return f;
+}
+RAX_HD int fast_quot(int n, FastDiv f) {
+  const unsigned x = f.mul ? (unsigned)(((unsigned long long)(unsigned)n * f.mul) >> 32) : (unsigned)n;
+  return (int)(x >> f.shift);
 }
 
 }  // namespace rax

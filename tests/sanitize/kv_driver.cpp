@@ -279,11 +279,11 @@ static void index_walk() {
 static void share_walk() {
   std::mt19937 g(11);
   for (int i = 0; i < 3000; ++i) {
-    const long long work = 1 + (i % 3 ? g() % 500 : (long long)g() << (g() % 20));
-    const int n = 1 + (int)(g() % std::min<long long>(work, 512));
+    const int work = 1 + (int)(i % 3 ? g() % 500 : g() % INT_MAX);
+    const int n = 1 + (int)(g() % std::min(work, 512));
     TRUE(rax::share_start(work, n, 0) == 0 && rax::share_start(work, n, n) == work);
     for (int b = 0; b < n; ++b) {
-      const long long x0 = rax::share_start(work, n, b), x1 = rax::share_start(work, n, b + 1);
+      const int x0 = rax::share_start(work, n, b), x1 = rax::share_start(work, n, b + 1);
       TRUE(x1 > x0 && x1 - x0 <= work / n + 1);
       TRUE(rax::share_owner(work, n, x0) == b && rax::share_owner(work, n, x1 - 1) == b);
     }
@@ -291,14 +291,28 @@ static void share_walk() {
   for (int i = 0; i < 20000; ++i) {
     const int max_len = i % 2 ? 16 * (1 + (int)(g() % 40)) : INT_MAX / 16 * 16, T = 1 + (int)(g() % 50);
     const rax::SeqRows s = rax::seq_rows((int)(g() % 60), (int)(g() % 60), (int)(g() % 3 ? g() % 700 : g()), T, max_len);
-    const int window = g() % 2 ? 0 : (int)(g() % 3 ? g() % 300 : g() >> 1), step = 16 << (g() % 4);
-    const rax::SeqSpan x = rax::seq_span(s, window, step);
+    const int window = g() % 2 ? 0 : (int)(g() % 3 ? g() % 300 : g() >> 1), step_log2 = 4 + g() % 5, step = 1 << step_log2;
+    const rax::SeqSpan x = rax::seq_span(s, window, step_log2);
     TRUE((x.steps == 0) == (s.n == 0) && x.base % 16 == 0);
     for (int t = 0; t < s.n; ++t) {
       const rax::KeyRange k = rax::token_keys(t, s.n, s.len, window);
       if (k.hi > k.lo) TRUE((unsigned)k.lo >= x.base && (unsigned)k.hi <= x.base + (unsigned long long)x.steps * step);
     }
     if (x.steps > 1) TRUE(x.base + (unsigned long long)(x.steps - 1) * step < (unsigned)s.len);
+  }
+  for (int d = 1; d <= 1024; ++d) {
+    const rax::FastDiv f = rax::fast_div(d);
+    for (int n : {0, 1, d - 1, d, d + 1, 5 * d - 1, 5 * d, 12345 * d - 1, 12345 * d, (1 << 30) / d * d, (1 << 30) / d * d - 1,
+                  1 << 30, INT_MAX, INT_MAX / d * d - 1, INT_MAX / d * d})
+      TRUE(rax::fast_quot(n, f) == n / d);
+  }
+  for (int i = 0; i < 3000; ++i) {   // the line fits 31 bits, also with every sequence at its bounds
+    const int seqs = 1 + g() % LORA_MAX_SEQS, group = 1 + g() % 1024, heads = 1 + g() % 1024, rows_log2 = 4 + g() % 4;
+    const int T = 1 + (int)(g() % std::min(1 << 24, (1 << 30) / group)), max_len = 1 + (int)(g() % INT_MAX);
+    const int step = rax::line_step_log2(5, seqs, T, max_len, heads, group, rows_log2);
+    if ((double)seqs * heads * rax::row_blocks(T, group, rows_log2) * 2.0 >= 2147483648.0) continue;   // step 31: refused
+    const rax::SeqSpan x = rax::seq_span(rax::SeqRows{0, T, max_len}, 0, step);
+    TRUE((double)x.steps * seqs * heads * rax::row_blocks(T, group, rows_log2) < 2147483648.0);
   }
   for (long long rows : {1LL, 16LL, 17LL, 33LL, 65LL, 1LL << 30}) {
     const rax::AttnRows r = rax::attention_rows(rows);
