@@ -476,9 +476,10 @@ typedef struct lora_kv_cache {
  * num_tokens positions[t] = past + index in the request and slots[t] (-1 for refused
  * requests); tokens past the batch's last get position 0 and slot -1, so a step of fixed size can be
  * padded.  cursor_out[0..1] = the ring after the step; cursor_out may be cursor (a step
- * replayed from a graph then advances).  cursor[2] is a scratch word of the call, zero
- * between calls.  meta[LORA_PLAN_META] = tokens, pages taken, pages given back, requests
- * refused, invalid entries, free pages after, 0, 0.
+ * replayed from a graph then advances).  cursor[2] and cursor[3] are scratch words of the
+ * call, zero between calls.  meta[LORA_PLAN_META] = tokens, pages taken, pages given back,
+ * requests refused, invalid entries, free pages after, 0, 0.  No output may overlap
+ * another vector, past_lens and seq_lens among them (cursor_out and cursor apart).
  * Invalid entries: a negative past, new_lens below -1 (the request counts as having no
  * tokens) or past + new above max_pages * page_size (its tokens get slot -1, its length
  * 0); a page id outside [0, num_pages) in the ring or in an existing part of a row (the

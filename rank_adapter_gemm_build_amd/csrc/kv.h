@@ -32,6 +32,9 @@ struct RotaryArgs {
   CacheView c;
   int ldqkv, ldq, dtype, q_heads, num_tokens, rot, interleaved;
   float amplitude;
+  // set by the launcher: tokens of a workgroup; divisors of the item numbers
+  int tokens_wg;
+  FastDiv per_half, per_head, per_chunk, per_turned;
 };
 hipError_t launch_rotary_append(const RotaryArgs& a, hipStream_t stream, const KTimer& tm);
 

@@ -136,7 +136,7 @@ RAX_HD int share_owner(int work, int g, int x) {
   return (int)((unsigned)x < wide ? (unsigned)x / (q + 1u) : rem + ((unsigned)x - wide) / q);
 }
 
-// Division by a fixed d in [1, 1024] of numbers below 2^31: with s = floor(log2 d), n / d =
+// Division by a fixed d in [1, 2^16] of numbers below 2^31: with s = floor(log2 d), n / d =
 // (n ceil(2^(32 + s) / d)) >> (32 + s), as the multiplier's excess, below d < 2^(s + 1),
 // times n stays below 2^(32 + s); a power of two is the shift alone (mul 0).
 struct FastDiv {

@@ -5,92 +5,237 @@
 // b sin, a sin + b cos).  f_i is kept in turns a position in 64 bits, so the angle's whole
 // turns drop out exactly (p f_i - round(p f_i)) and the remaining fraction, at most half a
 // turn, is good to 2^-26 of a turn in fp32 at any 31-bit position.
+//
+// What bounds it: reading the rows and writing q and the cells once.  The cosines of a
+// token serve all of its heads, so a workgroup takes whole tokens (several of a few short
+// heads) and keeps them in LDS; its loads are on their way while they are computed.
+// Everything moves in chunks of 8 values, two a thread and item:
+//   - pairs (2i, 2i + 1): 16 consecutive values, whose pairs lie within them;
+//   - pairs (i, i + half), half a multiple of 8: a chunk and the one half away;
+//   - any other half: the chunks' partners are not aligned, so the turned heads go through
+//     LDS, kRotarySlice bytes of heads at a time, and are picked up value by value.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "device_util.h"
 #include "kv.h"
 
 namespace rax {
 
-constexpr int kRotaryThreads = 256;
+constexpr int kRotaryThreads = 256, kRotaryTokens = 16, kRotarySlice = 16384;
 
-__device__ __forceinline__ float load_act(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-__device__ __forceinline__ float load_act(const float* p) { return *p; }
-__device__ __forceinline__ void store_act(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16(v); }
-__device__ __forceinline__ void store_act(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_cell(uint16_t* p, float v, float) { store_act(p, v); }
-__device__ __forceinline__ void store_cell(float* p, float v, float) { *p = v; }
-__device__ __forceinline__ void store_cell(uint8_t* p, float v, float scale) {
-  *p = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(fp8_clamp(v / scale), 0.f, 0, false);
+// 8 values: kept as they were read until they are used
+template <typename T> struct Chunk8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T> __device__ __forceinline__ Chunk8<T> load_chunk(const T* p) {
+  Chunk8<T> c;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) c.v[i] = ld16(reinterpret_cast<const char*>(p) + 16 * i);
+  return c;
 }
+__device__ __forceinline__ void to_floats(const Chunk8<uint16_t>& c, float (&x)[8]) { unpack8(c.v[0], x); }
+__device__ __forceinline__ void to_floats(const Chunk8<float>& c, float (&x)[8]) {
+  x[0] = __uint_as_float(c.v[0].x); x[1] = __uint_as_float(c.v[0].y); x[2] = __uint_as_float(c.v[0].z); x[3] = __uint_as_float(c.v[0].w);
+  x[4] = __uint_as_float(c.v[1].x); x[5] = __uint_as_float(c.v[1].y); x[6] = __uint_as_float(c.v[1].z); x[7] = __uint_as_float(c.v[1].w);
+}
+__device__ __forceinline__ void store_cells(uint16_t* p, const float (&x)[8], float) { store8f(p, x); }
+__device__ __forceinline__ void store_cells(float* p, const float (&x)[8], float) { store8f(p, x); }
+__device__ __forceinline__ void store_cells(uint8_t* p, const float (&x)[8], float scale) {
+  int w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(fp8_clamp(x[4 * i] / scale), fp8_clamp(x[4 * i + 1] / scale), 0, false);
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(fp8_clamp(x[4 * i + 2] / scale), fp8_clamp(x[4 * i + 3] / scale), w[i], true);
+  }
+  *reinterpret_cast<uint2*>(p) = make_uint2((uint32_t)w[0], (uint32_t)w[1]);
+}
+__device__ __forceinline__ float one_float(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ float one_float(const float* p) { return *p; }
 
-// T: activations, C: cache.  One workgroup a token.
-template <typename T, typename C>
+enum RotaryPairs { kInterleaved, kHalves, kOddHalves };
+
+// T: activations, C: cache
+template <typename T, typename C, int PAIRS>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_append_kernel(RotaryArgs a) {
-  __shared__ float cs[LORA_MAX_HEAD_DIM / 2], sn[LORA_MAX_HEAD_DIM / 2];
-  const int t = blockIdx.x, tid = threadIdx.x, D = a.c.dim, half = a.rot / 2;
-  const double p = a.positions[t];
-  for (int i = tid; i < half; i += kRotaryThreads) {
-    double x = p * a.turns[i];
-    x -= rint(x);
-    if constexpr (sizeof(T) == 4) {
-      double s, c;
-      sincospi(2.0 * x, &s, &c);
-      cs[i] = (float)c * a.amplitude;
-      sn[i] = (float)s * a.amplitude;
-    } else {
-      float s, c;
-      sincospif(2.0f * (float)x, &s, &c);
-      cs[i] = c * a.amplitude;
-      sn[i] = s * a.amplitude;
+  __shared__ float2 turn[kRotaryTokens * LORA_MAX_HEAD_DIM / 2];   // cos, sin of [token][pair]
+  __shared__ int slot_s[kRotaryTokens];
+  __shared__ uint4 slice[PAIRS == kOddHalves ? kRotarySlice / 16 : 1];
+  const int tid = threadIdx.x, D = a.c.dim, half = a.rot / 2, turned = a.q_heads + a.c.heads;
+  const int t0 = blockIdx.x * a.tokens_wg, tokens = min(a.tokens_wg, a.num_tokens - t0);
+
+  auto fill_turns = [&]() {
+    for (int e = tid; e < tokens * half; e += kRotaryThreads) {
+      const int t = fast_quot(e, a.per_half), i = e - t * half;
+      double x = (double)a.positions[t0 + t] * a.turns[i];
+      x -= rint(x);
+      if constexpr (sizeof(T) == 4) {
+        double s, c;
+        sincospi(2.0 * x, &s, &c);
+        turn[e] = make_float2((float)c * a.amplitude, (float)s * a.amplitude);
+      } else {
+        float s, c;
+        sincospif(2.0f * (float)x, &s, &c);
+        turn[e] = make_float2(c * a.amplitude, s * a.amplitude);
+      }
     }
-  }
-  __syncthreads();
-  const int slot = a.slots[t], page = slot >> a.c.page_shift, off = slot & ((1 << a.c.page_shift) - 1);
-  const bool stored = slot >= 0 && page < a.c.num_pages;
-  const long long row = stored ? page * a.c.page_stride + off * a.c.token_stride : 0;
-  const T* in = reinterpret_cast<const T*>(a.qkv) + (size_t)t * a.ldqkv;
-  T* q = reinterpret_cast<T*>(a.q_out) + (size_t)t * a.ldq;
-  C *kc = reinterpret_cast<C*>(a.c.k) + row, *vc = reinterpret_cast<C*>(a.c.v) + row;
-  const int turned = a.q_heads + a.c.heads, per = D - half;   // items of a head: pairs, then single values
-  for (int e = tid; e < turned * per; e += kRotaryThreads) {
-    const int h = e / per, i = e - h * per;
-    int d0, d1 = -1;
-    float x, y = 0.f;
-    if (i < half) {
-      d0 = a.interleaved ? 2 * i : i;
-      d1 = a.interleaved ? 2 * i + 1 : i + half;
-      const float u = load_act(in + h * D + d0), w = load_act(in + h * D + d1);
-      x = u * cs[i] - w * sn[i];
-      y = u * sn[i] + w * cs[i];
-    } else {
-      d0 = i + half;
-      x = load_act(in + h * D + d0);
-    }
+    if (tid < tokens) slot_s[tid] = a.slots[t0 + tid];
+  };
+  auto put = [&](int t, int h, int d, const float (&x)[8]) {
     if (h < a.q_heads) {
-      store_act(q + h * D + d0, x);
-      if (d1 >= 0) store_act(q + h * D + d1, y);
-    } else if (stored) {
-      C* k = kc + (h - a.q_heads) * a.c.head_stride;
-      store_cell(k + d0, x, a.c.k_scale);
-      if (d1 >= 0) store_cell(k + d1, y, a.c.k_scale);
+      store8f(reinterpret_cast<T*>(a.q_out) + (size_t)(t0 + t) * a.ldq + h * D + d, x);
+      return;
+    }
+    const int slot = slot_s[t], page = slot >> a.c.page_shift;
+    if (slot < 0 || page >= a.c.num_pages) return;
+    const bool key = h < turned;
+    C* p = reinterpret_cast<C*>(key ? a.c.k : a.c.v) + page * a.c.page_stride +
+           (slot & ((1 << a.c.page_shift) - 1)) * a.c.token_stride + (h - (key ? a.q_heads : turned)) * a.c.head_stride + d;
+    store_cells(p, x, key ? a.c.k_scale : a.c.v_scale);
+  };
+  const T* rows = reinterpret_cast<const T*>(a.qkv);
+  const int per_head = D / 16, heads = turned + a.c.heads;
+
+  // items of two chunks, from head h0 on
+  auto direct = [&](int h0, auto before_use) {
+    const int per_token = (heads - h0) * per_head, items = tokens * per_token;
+    constexpr int U = 2;
+    bool first = true;
+    for (int e0 = tid; first || e0 < items; e0 += U * kRotaryThreads) {
+      Chunk8<T> c[U][2];
+      int tt[U], hh[U], d0[U], d1[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int e = e0 + u * kRotaryThreads;
+        tt[u] = -1;
+        if (e < items) {
+          tt[u] = tokens == 1 ? 0 : e / per_token;
+          const int j = e - tt[u] * per_token, h = fast_quot(j, a.per_head), i = j - h * per_head;
+          hh[u] = h0 + h;
+          d0[u] = 16 * i;
+          d1[u] = 16 * i + 8;
+          if (PAIRS == kHalves && hh[u] < turned) {
+            const bool pair = 8 * i < half;
+            d0[u] = pair ? 8 * i : 16 * i;      // half / 8 items hold pairs, so value 16 i
+            d1[u] = pair ? half + 8 * i : 16 * i + 8;   // is the first of the next ones
+          }
+          const T* p = rows + (size_t)(t0 + tt[u]) * a.ldqkv + hh[u] * D;
+          c[u][0] = load_chunk(p + d0[u]);
+          c[u][1] = load_chunk(p + d1[u]);
+        }
+      }
+      if (first) before_use();
+      first = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (tt[u] < 0) continue;
+        float x[8], y[8];
+        to_floats(c[u][0], x);
+        to_floats(c[u][1], y);
+        if (hh[u] < turned) {
+          const float2* cs = turn + tt[u] * half;
+          if constexpr (PAIRS == kHalves) {
+            if (d0[u] < half)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float2 r = cs[d0[u] + k];
+                const float v = x[k], w = y[k];
+                x[k] = v * r.x - w * r.y;
+                y[k] = v * r.y + w * r.x;
+              }
+          } else if constexpr (PAIRS == kInterleaved) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+              const int i = d0[u] / 2 + k / 2;
+              if (i < half) {
+                const float2 r = cs[i];
+                const float v = x[k], w = x[k + 1];
+                x[k] = v * r.x - w * r.y;
+                x[k + 1] = v * r.y + w * r.x;
+              }
+              if (i + 4 < half) {
+                const float2 r = cs[i + 4];
+                const float v = y[k], w = y[k + 1];
+                y[k] = v * r.x - w * r.y;
+                y[k + 1] = v * r.y + w * r.x;
+              }
+            }
+          }
+        }
+        put(tt[u], hh[u], d0[u], x);
+        put(tt[u], hh[u], d1[u], y);
+      }
+    }
+  };
+  if constexpr (PAIRS != kOddHalves) {
+    direct(0, [&]() {
+      fill_turns();
+      __syncthreads();
+    });
+  } else {
+    direct(turned, [&]() {
+      fill_turns();
+      __syncthreads();
+    });
+    // turned heads: slices of whole heads through LDS
+    const T* in = reinterpret_cast<const T*>(slice);
+    const int slice_heads = kRotarySlice / (D * (int)sizeof(T)), chunks_head = D / 8, all = tokens * turned;
+    for (int g0 = 0; g0 < all; g0 += slice_heads) {
+      const int n = min(slice_heads, all - g0);
+      for (int e = tid; e < n * chunks_head; e += kRotaryThreads) {
+        const int g = fast_quot(e, a.per_chunk), t = fast_quot(g0 + g, a.per_turned), h = g0 + g - t * turned;
+        const Chunk8<T> c = load_chunk(rows + (size_t)(t0 + t) * a.ldqkv + h * D + (e - g * chunks_head) * 8);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) slice[e * ((int)sizeof(T) / 2) + i] = c.v[i];
+      }
+      __syncthreads();   // the whole slice is read: q_out may be the rows themselves
+      for (int e = tid; e < n * chunks_head; e += kRotaryThreads) {
+        const int g = fast_quot(e, a.per_chunk), t = fast_quot(g0 + g, a.per_turned), h = g0 + g - t * turned;
+        const int d = (e - g * chunks_head) * 8;
+        const T* head = in + g * D;
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int dk = d + k, i = dk < half ? dk : dk - half;
+          x[k] = one_float(head + dk);
+          if (dk < a.rot) {
+            const float2 r = turn[t * half + i];
+            const float w = one_float(head + (dk < half ? dk + half : i));
+            x[k] = dk < half ? x[k] * r.x - w * r.y : w * r.y + x[k] * r.x;
+          }
+        }
+        put(t, h, d, x);
+      }
+      __syncthreads();
     }
   }
-  if (stored)
-    for (int e = tid; e < a.c.heads * D; e += kRotaryThreads) {
-      const int h = e / D, d = e - h * D;
-      store_cell(vc + h * a.c.head_stride + d, load_act(in + turned * D + e), a.c.v_scale);
-    }
 }
 
-hipError_t launch_rotary_append(const RotaryArgs& a, hipStream_t stream, const KTimer& tm) {
-  const dim3 grid(a.num_tokens), block(kRotaryThreads);
+template <int PAIRS>
+static void launch_pairs(const RotaryArgs& a, const dim3& grid, hipStream_t stream, const KTimer& tm) {
+  const dim3 block(kRotaryThreads);
   if (a.dtype == LORA_F32)
-    RAX_LAUNCH(tm, (rotary_append_kernel<float, float>), grid, block, 0u, stream, a);
+    RAX_LAUNCH(tm, (rotary_append_kernel<float, float, PAIRS>), grid, block, 0u, stream, a);
   else if (a.c.dtype == LORA_FP8E4M3)
-    RAX_LAUNCH(tm, (rotary_append_kernel<uint16_t, uint8_t>), grid, block, 0u, stream, a);
+    RAX_LAUNCH(tm, (rotary_append_kernel<uint16_t, uint8_t, PAIRS>), grid, block, 0u, stream, a);
   else
-    RAX_LAUNCH(tm, (rotary_append_kernel<uint16_t, uint16_t>), grid, block, 0u, stream, a);
+    RAX_LAUNCH(tm, (rotary_append_kernel<uint16_t, uint16_t, PAIRS>), grid, block, 0u, stream, a);
+}
+
+hipError_t launch_rotary_append(const RotaryArgs& args, hipStream_t stream, const KTimer& tm) {
+  RotaryArgs a = args;
+  const int items = (a.q_heads + 2 * a.c.heads) * (a.c.dim / 16);
+  // two items a thread, as long as the chip stays full of workgroups
+  a.tokens_wg = std::max(1, std::min({kRotaryTokens, 2 * kRotaryThreads / items, a.num_tokens / 1024}));
+  a.per_half = fast_div(a.rot / 2);
+  a.per_head = fast_div(a.c.dim / 16);
+  a.per_chunk = fast_div(a.c.dim / 8);
+  a.per_turned = fast_div(a.q_heads + a.c.heads);
+  const dim3 grid((a.num_tokens + a.tokens_wg - 1) / a.tokens_wg);
+  if (a.interleaved) launch_pairs<kInterleaved>(a, grid, stream, tm);
+  else if (a.rot % 16 == 0) launch_pairs<kHalves>(a, grid, stream, tm);
+  else launch_pairs<kOddHalves>(a, grid, stream, tm);
   return hipGetLastError();
 }
 

@@ -24,16 +24,31 @@ __all__ = ["LORA_MAX_SEQS", "LORA_MAX_HEAD_DIM", "LORA_PLAN_META", "LORA_ROPE_PL
            "page_plan", "rotary_append", "paged_attention"]
 
 
+# A call of a small step costs the host more than the GPU, so the checks read each property of a
+# tensor once and torch is looked up once.
+torch = None          # the module, from the first object or call on
+_raw_stream = None    # device -> raw handle of its current stream
+
+
+def _load() -> None:
+    global torch, _raw_stream
+    import torch as module
+
+    def public(device):
+        return module.cuda.current_stream(device).cuda_stream
+    _raw_stream = getattr(module._C, "_cuda_getCurrentRawStream", public)
+    torch = module
+
+
 def _stream_on(device: int, stream) -> Optional[int]:
     """Raw stream: the given one, or `device`'s current stream."""
     if stream is None:
-        import torch
-        return torch.cuda.current_stream(device).cuda_stream or None
+        return _raw_stream(device) or None
     return (stream if isinstance(stream, int) else stream.cuda_stream) or None
 
 
-def _on(device: int, *named) -> None:
-    """The device rule, checked after every other rule of a call."""
+def _elsewhere(device: int, *named) -> None:
+    """The device rule's error, for the first tensor that breaks it."""
     for what, t in named:
         if t.get_device() != device:
             raise ValueError(f"{what} must be a tensor on cuda:{device}")
@@ -41,10 +56,9 @@ def _on(device: int, *named) -> None:
 
 def _vec(t, least: int, what: str) -> int:
     """Address of a contiguous int32 vector of at least `least` entries."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch tensor")
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{what} must be int32 (got {t.dtype})")
     if t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous 1-D tensor")
@@ -55,17 +69,18 @@ def _vec(t, least: int, what: str) -> int:
 
 def _table(t, rows: int) -> tuple:
     """(address, row stride, columns) of a block table."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError("block_table must be a torch tensor")
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"block_table must be int32 (got {t.dtype})")
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < 1:
-        raise ValueError(f"block_table must be 2-D with at least {rows} rows and a column (got {tuple(t.shape)})")
-    ld, cols = t.stride(0), t.shape[1]
-    if cols > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] < 1:
+        raise ValueError(f"block_table must be 2-D with at least {rows} rows and a column (got {tuple(shape)})")
+    cols = shape[1]
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
         raise ValueError("block_table must have unit column stride")
-    if t.shape[0] == 1:
+    if shape[0] == 1:
         ld = max(ld, cols)
     elif ld < cols:
         raise ValueError(f"block_table: row stride {ld} is below its width {cols}")
@@ -74,15 +89,14 @@ def _table(t, rows: int) -> tuple:
 
 def _rows(t, dtype, rows: int, width: int, what: str) -> tuple:
     """(address, row stride) of a row-major [rows, width] matrix."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype} (got {t.dtype})")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+    if t.shape != (rows, width):
         raise ValueError(f"{what} must have shape ({rows}, {width}) (got {tuple(t.shape)})")
-    ld = t.stride(0)
-    if t.stride(1) != 1 and width > 1:
+    ld, unit = t.stride()
+    if unit != 1 and width > 1:
         raise ValueError(f"{what} must have unit column stride (got stride {t.stride()})")
     if rows <= 1:
         ld = -(-max(ld, width) // 8) * 8   # the stride of a single row is never used
@@ -98,7 +112,8 @@ class KVCache:
     Holds references to the tensors; see lora_kv_cache for the rules."""
 
     def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0):
-        import torch
+        if torch is None:
+            _load()
         for t, what in ((k, "k"), (v, "v")):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{what} must be a torch tensor")
@@ -121,7 +136,7 @@ class KVCache:
             raise ValueError("k and v must have the same strides")
         if dtype == LORA_FP8E4M3 and not all(math.isfinite(s) and s > 0 for s in (k_scale, v_scale)):
             raise ValueError("k_scale and v_scale must be positive and finite")
-        self.k, self.v, self.dtype = k, v, dtype
+        self.k, self.v, self.dtype, self.device = k, v, dtype, k.get_device()
         self.num_pages, self.page_size, self.num_heads, self.head_dim = pages, size, heads, dim
         self.act = torch.float32 if dtype == LORA_F32 else torch.bfloat16   # the activations it takes
         self.act_code = LORA_F32 if dtype == LORA_F32 else LORA_BF16
@@ -136,7 +151,8 @@ class PagePlan:
     META = ("tokens", "pages_taken", "pages_returned", "refused", "invalid", "free_pages")
 
     def __init__(self, device: int, max_seqs: int, max_tokens: int):
-        import torch
+        if torch is None:
+            _load()
         if not 0 <= max_seqs <= LORA_MAX_SEQS or max_tokens < 0:
             raise ValueError(f"max_seqs must be in [0, {LORA_MAX_SEQS}] and max_tokens not negative")
         self.device, self.max_seqs, self.max_tokens = device, max_seqs, max_tokens
@@ -159,6 +175,8 @@ def page_plan(plan: PagePlan, past_lens, new_lens, num_tokens: int, free_pages, 
     plan.positions and plan.slots to fill (the batch's tokens, or more for a padded step);
     free_pages: int32 ring [num_pages]; cursor: int32 [4] (first free place, free pages, 0,
     0); cursor_out: where the advanced cursor goes (default: cursor itself)."""
+    if torch is None:
+        _load()
     dev = plan.device
     past = _vec(past_lens, 0, "past_lens")
     n = past_lens.numel()
@@ -172,8 +190,11 @@ def page_plan(plan: PagePlan, past_lens, new_lens, num_tokens: int, free_pages, 
     ring, cur = _vec(free_pages, 1, "free_pages"), _vec(cursor, 4, "cursor")
     cur_out = cur if cursor_out is None else _vec(cursor_out, 2, "cursor_out")
     table, ld, cols = _table(block_table, n)
-    _on(dev, ("past_lens", past_lens), ("new_lens", new_lens), ("free_pages", free_pages), ("cursor", cursor),
-        ("block_table", block_table), ("cursor_out", cursor if cursor_out is None else cursor_out))
+    if (past_lens.get_device() != dev or new_lens.get_device() != dev or free_pages.get_device() != dev or
+            cursor.get_device() != dev or block_table.get_device() != dev or
+            (cursor_out is not None and cursor_out.get_device() != dev)):
+        _elsewhere(dev, ("past_lens", past_lens), ("new_lens", new_lens), ("free_pages", free_pages), ("cursor", cursor),
+                   ("block_table", block_table), ("cursor_out", cursor_out))
     lens, starts, positions, slots, meta = plan._out
     _check(lib.lora_page_plan(dev, past, new, n, num_tokens, page_size, free_pages.numel(), ring, cur, cur_out, table, ld,
                               cols, lens, starts, positions, slots, meta, _stream_on(dev, stream)), "lora_page_plan")
@@ -223,12 +244,16 @@ def rotary_append(rotary: Rotary, qkv, num_q_heads: int, positions, slots, q_out
     """q_out = the turned q heads of the packed rows qkv [T, (num_q_heads + 2 num_heads) *
     head_dim]; the turned k heads and the v heads go to the cache at `slots` (see
     lora_rotary_append).  q_out [T, num_q_heads * head_dim] may be qkv's own first columns."""
+    if torch is None:
+        _load()
     dev, dim = rotary.device, cache.head_dim
     T = qkv.shape[0] if hasattr(qkv, "shape") and len(qkv.shape) else 0
     x, ldx = _rows(qkv, cache.act, T, (num_q_heads + 2 * cache.num_heads) * dim, "qkv")
     q, ldq = _rows(q_out, cache.act, T, num_q_heads * dim, "q_out")
     pos, sl = _vec(positions, T, "positions"), _vec(slots, T, "slots")
-    _on(dev, ("qkv", qkv), ("q_out", q_out), ("positions", positions), ("slots", slots), ("the cache", cache.k))
+    if (qkv.get_device() != dev or q_out.get_device() != dev or positions.get_device() != dev or
+            slots.get_device() != dev or cache.device != dev):
+        _elsewhere(dev, ("qkv", qkv), ("q_out", q_out), ("positions", positions), ("slots", slots), ("the cache", cache.k))
     _check(lib.lora_rotary_append(rotary.handle, x or None, ldx, cache.act_code, num_q_heads, pos or None, sl or None, T,
                                   q or None, ldq, cache.ref, _stream_on(dev, stream)), "lora_rotary_append")
 
@@ -263,6 +288,8 @@ def paged_attention(attention: Attention, q, cache: KVCache, block_table, seq_le
     (see lora_paged_attention).  block_table, seq_lens, query_start: of the page plan or
     the caller's own, one row (entry) per sequence, query_start one longer; scale: default
     1 / sqrt(head_dim); window: keys a token sees, 0 for all; lse: float32 [T, num_q_heads]."""
+    if torch is None:
+        _load()
     dev = attention.device
     n = query_start.numel() - 1 if hasattr(query_start, "numel") else 0
     starts, lens = _vec(query_start, 1, "query_start"), _vec(seq_lens, n, "seq_lens")
@@ -273,13 +300,15 @@ def paged_attention(attention: Attention, q, cache: KVCache, block_table, seq_le
     op, ldo = _rows(out, cache.act, T, width, "out")
     lp = None
     if lse is not None:
-        import torch
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (T, attention.num_q_heads) or not lse.is_contiguous():
+        if lse.dtype is not torch.float32 or lse.shape != (T, attention.num_q_heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be a contiguous float32 tensor of shape ({T}, {attention.num_q_heads})")
-        _on(dev, ("lse", lse))
+        if lse.get_device() != dev:
+            _elsewhere(dev, ("lse", lse))
         lp = lse.data_ptr()
-    _on(dev, ("q", q), ("out", out), ("block_table", block_table), ("seq_lens", seq_lens), ("query_start", query_start),
-        ("the cache", cache.k))
+    if (q.get_device() != dev or out.get_device() != dev or block_table.get_device() != dev or
+            seq_lens.get_device() != dev or query_start.get_device() != dev or cache.device != dev):
+        _elsewhere(dev, ("q", q), ("out", out), ("block_table", block_table), ("seq_lens", seq_lens),
+                   ("query_start", query_start), ("the cache", cache.k))
     _check(lib.lora_paged_attention(attention.handle, qp or None, ldq, cache.act_code, cache.ref, table, ld, cols,
                                     lens, starts, n, T, 1.0 / math.sqrt(attention.head_dim) if scale is None else scale,
                                     window, op or None, ldo, lp or None, _stream_on(dev, stream)), "lora_paged_attention")
