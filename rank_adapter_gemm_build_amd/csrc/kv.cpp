@@ -27,15 +27,12 @@ struct lora_rotary {
 
 struct lora_attention {
   int device = 0, max_seqs = 0, max_tokens = 0, q_heads = 0, kv_heads = 0, dim = 0;
-  int workers = 0, part_rows = 0;
+  int workers = 0;                               // workgroups of 4 waves
   float *part_o = nullptr, *part_ml = nullptr;   // device
   int* arrived = nullptr;                        // device, zero between calls
 };
 
 namespace rax {
-// Rows (new tokens times query heads of a kv head) that a workgroup takes of a sequence:
-// as many of its waves share rows as the mean sequence of the batch fills; the other waves
-// split the keys.
 AttnRows attention_rows(long long rows) {
   if (rows <= 16) return {1, 1};
   if (rows <= 32) return {2, 1};
@@ -320,18 +317,20 @@ lora_status lora_attention_create(lora_attention** out, int device, int max_seqs
   if (!a) return fail(LORA_ERR_OOM, "out of host memory");
   a->device = device;
   // two workgroups a compute unit fit in registers and LDS
-  a->workers = std::min(rax::kMaxParts, std::max(8, 2 * cus / 8 * 8));
-  a->part_rows = rax::attention_rows((long long)max_tokens * (num_q_heads / num_kv_heads)).rows();
+  a->workers = std::min(512, std::max(8, 2 * cus / 8 * 8));
   a->max_seqs = max_seqs;
   a->max_tokens = max_tokens;
   a->q_heads = num_q_heads;
   a->kv_heads = num_kv_heads;
   a->dim = head_dim;
-  const size_t part = 2 * (size_t)a->workers * a->part_rows * sizeof(float);
+  // two slots a workgroup; one-wave workgroups have 16 rows, and there are 4 times as many
+  const size_t rows = rax::attention_rows((long long)max_tokens * (num_q_heads / num_kv_heads)).rows();
+  const size_t part = 2 * (size_t)a->workers * std::max<size_t>(rows, 4 * 16) * sizeof(float);
+  const size_t counters = sizeof(int) * rax::kJoinLevels * 4 * a->workers;
   e = hipMalloc(reinterpret_cast<void**>(&a->part_o), part * head_dim);
   if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->part_ml), part * 2);
-  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->arrived), a->workers * sizeof(int));
-  if (e == hipSuccess) e = hipMemset(a->arrived, 0, a->workers * sizeof(int));
+  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->arrived), counters);
+  if (e == hipSuccess) e = hipMemset(a->arrived, 0, counters);
   if (e == hipSuccess) e = hipDeviceSynchronize();
   if (e != hipSuccess) {
     (void)lora_attention_destroy(a);
@@ -398,20 +397,22 @@ lora_status lora_paged_attention(const lora_attention* attention, const void* q,
   a.max_pages = max_pages;
   a.window = window;
   a.scale = scale;
-  const rax::AttnRows rows =
-      rax::attention_rows(((long long)num_tokens + num_seqs - 1) / num_seqs * (attention->q_heads / attention->kv_heads));
-  a.row_tiles = rows.tiles;
-  a.row_waves = rows.waves;
-  a.workers = attention->workers;
-  a.min_steps = 2;
   a.group_size = attention->q_heads / attention->kv_heads;
   a.group = rax::fast_div(a.group_size);
-  a.step_log2 = rax::line_step_log2(rax::attention_step_log2(a), num_seqs, num_tokens, max_pages * cache->page_size,
-                                    attention->kv_heads, a.group_size, log2_of(rows.rows()));
-  a.part_rows = attention->part_rows;
+  const long long mean_rows = ((long long)num_tokens + num_seqs - 1) / num_seqs * a.group_size;
+  const rax::AttnRows rows = rax::attention_rows(mean_rows);
+  a.row_tiles = rows.tiles;
+  a.row_waves = rows.waves;
+  a.waves = rows.rows() == 16 && (long long)num_seqs * attention->kv_heads >= 2 * attention->workers ? 1 : 4;
+  a.workers = attention->workers * (4 / a.waves);
+  a.step_log2 = rax::attention_step_log2(a);
+  a.min_steps = std::max(1, (int)std::min(8 * mean_rows, 1024LL) >> a.step_log2);
+  a.step_log2 = rax::line_step_log2(a.step_log2, num_seqs, num_tokens, max_pages * cache->page_size, attention->kv_heads,
+                                    a.group_size, log2_of(rows.rows()));
   a.part_o = attention->part_o;
   a.part_ml = attention->part_ml;
   a.arrived = attention->arrived;
+  a.counters = 4 * attention->workers;
   const hipError_t e = rax::launch_paged_attention(a, stream, timer_for(rax::kKAttention));
   if (e != hipSuccess) return hip_fail(e, "paged attention launch");
   return ok();

@@ -47,27 +47,27 @@ struct AttentionArgs {
   int ldq, ldo, dtype, q_heads, num_seqs, num_tokens, ld_table, max_pages, window;
   float scale;
   // the launch's shape and workspace
-  int row_tiles, row_waves;   // rows of a workgroup: 16 * row_tiles * row_waves
-  int workers, min_steps;     // workgroups; steps each has at least
-  int step_log2;              // keys of a step
-  int group_size;             // query heads of a kv head
+  int waves, row_tiles, row_waves;   // of a workgroup; its rows: 16 * row_tiles * row_waves
+  int workers, min_steps;            // workgroups; steps each has at least
+  int step_log2;                     // keys of a step
+  int group_size;                    // query heads of a kv head
   FastDiv group;
-  int part_rows;              // rows of a slot of part_o and part_ml
-  float *part_o, *part_ml;    // two slots a workgroup: [part_rows][dim], [part_rows][2]
-  int* arrived;               // a counter a workgroup, zero between launches
+  float *part_o, *part_ml;           // two slots a workgroup: [rows][dim], [rows][2]
+  int *arrived, counters;            // [kJoinLevels][counters], zero between launches
 };
-// workgroups a launch has at most (the join keeps a weight of each in LDS), a multiple of 8
-constexpr int kMaxParts = 512;
+constexpr int kJoinLevels = 4;       // 8^4 parts of a unit: more than there are workgroups
+// Shape of a workgroup by the rows (new tokens times query heads of a kv head) that the mean
+// sequence has: as many of its waves share rows as those fill, the others split the keys.
 struct AttnRows {
   int tiles, waves;
   int rows() const { return 16 * tiles * waves; }
 };
 AttnRows attention_rows(long long rows);
-// keys that a workgroup's waves take at a time (log2): 16 (fp32) or 32 each, the waves that
-// do not share rows side by side
+// keys that a workgroup's waves take at a time (log2): a tile each, the waves that do not
+// share rows side by side
 inline int attention_step_log2(const AttentionArgs& a) {
-  int s = a.dtype == LORA_F32 ? 6 : 7;
-  for (int w = a.row_waves; w > 1; w /= 2) --s;
+  int s = a.dtype == LORA_F32 ? 4 : 5;
+  for (int w = a.waves / a.row_waves; w > 1; w /= 2) ++s;
   return s;
 }
 hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t stream, const KTimer& tm);
