@@ -253,8 +253,10 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
   if (work_ == 0) return;
   for (int i = r0; i < r1; ++i) sums[i] += before;
   const int workers_ = min((work_ + a.min_steps - 1) / a.min_steps, (int)gridDim.x);
-  // neighbouring shares on one XCD: the row blocks of a head read its keys from one L2
-  const int b_ = (int)(blockIdx.x % kXcds) * (int)(gridDim.x / kXcds) + (int)(blockIdx.x / kXcds);
+  // neighbouring shares on one XCD (the row blocks of a head read its keys from one L2), and
+  // as many on each
+  const int per_xcd = (workers_ + kXcds - 1) / kXcds, place = (int)(blockIdx.x / kXcds);
+  const int b_ = place < per_xcd ? (int)(blockIdx.x % kXcds) * per_xcd + place : workers_;
   if (b_ >= workers_) return;
   lds_barrier();
 
@@ -787,8 +789,7 @@ template <typename C, int DB> static void launch_rows(const AttentionArgs& a, hi
   if (a.waves == 1) launch_shape<C, DB, 1, 1, 1>(a, stream, tm);
   else if (a.row_tiles == 1) launch_shape<C, DB, 1, 4, 1>(a, stream, tm);
   else if (a.row_waves == 1) launch_shape<C, DB, 2, 4, 1>(a, stream, tm);
-  else if (a.row_waves == 2) launch_shape<C, DB, 2, 4, 2>(a, stream, tm);
-  else launch_shape<C, DB, 2, 4, 4>(a, stream, tm);
+  else launch_shape<C, DB, 2, 4, 2>(a, stream, tm);
 }
 template <typename C> hipError_t launch_attention_of(const AttentionArgs& a, hipStream_t stream, const KTimer& tm) {
   if (a.c.dim <= 64) launch_rows<C, 64>(a, stream, tm);

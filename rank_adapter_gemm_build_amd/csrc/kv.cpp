@@ -33,11 +33,15 @@ struct lora_attention {
 };
 
 namespace rax {
-AttnRows attention_rows(long long rows) {
-  if (rows <= 16) return {1, 1};
-  if (rows <= 32) return {2, 1};
-  if (rows <= 64) return {2, 2};
-  return {2, 4};
+// Larger blocks read the keys fewer times, but where there are few units each is cut into
+// many parts, whose join one workgroup does: the more blocks, the more of those.  Measured
+// with blocks of 64, 32, 16 rows: 64 rows of 32 x 8 heads 116, 114, 185 us, of 64 x 8 heads
+// 174, 213, 330; of 1 x 8 heads 77, 46, 31; 32 rows of 16 x 8 heads (-, 55, 62).  Four row
+// waves (128 rows) were slower than two everywhere (128 rows of 128 x 4 heads 205 us, 149).
+AttnRows attention_rows(long long rows, long long heads) {
+  if (rows > 32 && heads * ((rows + 63) / 64) >= 256) return {2, 2};
+  if (rows > 16 && heads * ((rows + 31) / 32) >= 128) return {2, 1};
+  return {1, 1};
 }
 }  // namespace rax
 
@@ -323,9 +327,8 @@ lora_status lora_attention_create(lora_attention** out, int device, int max_seqs
   a->q_heads = num_q_heads;
   a->kv_heads = num_kv_heads;
   a->dim = head_dim;
-  // two slots a workgroup; one-wave workgroups have 16 rows, and there are 4 times as many
-  const size_t rows = rax::attention_rows((long long)max_tokens * (num_q_heads / num_kv_heads)).rows();
-  const size_t part = 2 * (size_t)a->workers * std::max<size_t>(rows, 4 * 16) * sizeof(float);
+  // two slots a workgroup of at most 64 rows, or of 16 rows and one wave, 4 times as many
+  const size_t part = 2 * (size_t)a->workers * rax::kMaxRows * sizeof(float);
   const size_t counters = sizeof(int) * rax::kJoinLevels * 4 * a->workers;
   e = hipMalloc(reinterpret_cast<void**>(&a->part_o), part * head_dim);
   if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->part_ml), part * 2);
@@ -400,13 +403,19 @@ lora_status lora_paged_attention(const lora_attention* attention, const void* q,
   a.group_size = attention->q_heads / attention->kv_heads;
   a.group = rax::fast_div(a.group_size);
   const long long mean_rows = ((long long)num_tokens + num_seqs - 1) / num_seqs * a.group_size;
-  const rax::AttnRows rows = rax::attention_rows(mean_rows);
+  const rax::AttnRows rows = rax::attention_rows(mean_rows, (long long)num_seqs * attention->kv_heads);
   a.row_tiles = rows.tiles;
   a.row_waves = rows.waves;
-  a.waves = rows.rows() == 16 && (long long)num_seqs * attention->kv_heads >= 2 * attention->workers ? 1 : 4;
-  a.workers = attention->workers * (4 / a.waves);
+  // One wave a workgroup where there is a unit for most of the waves and the table's width
+  // bounds their keys: 256 sequences of 8 to 60 tokens took 22.1 us against 29.1, of 100 to
+  // 500 79.0 against 80.1; of 2000 to 4000, where the table is wider, 590 against 536.
+  a.waves = rows.rows() == 16 && (long long)num_seqs * attention->kv_heads >= 2 * attention->workers &&
+            (long long)max_pages * cache->page_size <= 1024 ? 1 : 4;
+  // two workgroups a compute unit fit in registers, above 128 dims one
+  a.workers = attention->workers * (4 / a.waves) / (attention->dim > 128 ? 2 : 1);
   a.step_log2 = rax::attention_step_log2(a);
-  a.min_steps = std::max(1, (int)std::min(8 * mean_rows, 1024LL) >> a.step_log2);
+  // at least so many keys a workgroup: fewer cost more in the join than they save
+  a.min_steps = a.waves == 1 ? 1 : std::max(1, std::max(128, 4 * rows.rows()) >> a.step_log2);
   a.step_log2 = rax::line_step_log2(a.step_log2, num_seqs, num_tokens, max_pages * cache->page_size, attention->kv_heads,
                                     a.group_size, log2_of(rows.rows()));
   a.part_o = attention->part_o;

@@ -57,12 +57,13 @@ struct AttentionArgs {
 };
 constexpr int kJoinLevels = 4;       // 8^4 parts of a unit: more than there are workgroups
 // Shape of a workgroup by the rows (new tokens times query heads of a kv head) that the mean
-// sequence has: as many of its waves share rows as those fill, the others split the keys.
+// sequence has, and the number of sequences times kv heads.
+constexpr int kMaxRows = 64;
 struct AttnRows {
-  int tiles, waves;
+  int tiles, waves;   // row tiles of a wave; waves that share the keys, the others split them
   int rows() const { return 16 * tiles * waves; }
 };
-AttnRows attention_rows(long long rows);
+AttnRows attention_rows(long long rows, long long heads);
 // keys that a workgroup's waves take at a time (log2): a tile each, the waves that do not
 // share rows side by side
 inline int attention_step_log2(const AttentionArgs& a) {

@@ -314,10 +314,11 @@ static void share_walk() {
     const rax::SeqSpan x = rax::seq_span(rax::SeqRows{0, T, max_len}, 0, step);
     TRUE((double)x.steps * seqs * heads * rax::row_blocks(T, group, rows_log2) < 2147483648.0);
   }
-  for (long long rows : {1LL, 16LL, 17LL, 33LL, 65LL, 1LL << 30}) {
-    const rax::AttnRows r = rax::attention_rows(rows);
-    TRUE(4 % r.waves == 0 && (rows > 128 || r.rows() >= rows) && r.rows() <= 128);
-  }
+  for (long long rows : {1LL, 16LL, 17LL, 33LL, 65LL, 1LL << 30})
+    for (long long heads : {1LL, 64LL, 128LL, 4096LL * 1024}) {
+      const rax::AttnRows r = rax::attention_rows(rows, heads);
+      TRUE(4 % r.waves == 0 && r.rows() <= rax::kMaxRows && (r.rows() == 16 || 2 * rows > r.rows()));
+    }
 }
 
 int main() {
