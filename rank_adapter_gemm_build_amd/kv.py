@@ -56,53 +56,57 @@ def _elsewhere(device: int, *named) -> None:
 
 def _vec(t, least: int, what: str) -> int:
     """Address of a contiguous int32 vector of at least `least` entries."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a torch tensor")
-    if t.dtype is not torch.int32:
-        raise TypeError(f"{what} must be int32 (got {t.dtype})")
-    if t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous 1-D tensor")
-    if t.numel() < least:
-        raise ValueError(f"{what} must have at least {least} entries (got {t.numel()})")
-    return t.data_ptr()
+    try:
+        if t.dtype is not torch.int32:
+            raise TypeError(f"{what} must be an int32 torch tensor (got {t.dtype})")
+        shape = t.shape
+        if len(shape) != 1 or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous 1-D tensor")
+        if shape[0] < least:
+            raise ValueError(f"{what} must have at least {least} entries (got {shape[0]})")
+        return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{what} must be a torch tensor") from None
 
 
 def _table(t, rows: int) -> tuple:
     """(address, row stride, columns) of a block table."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("block_table must be a torch tensor")
-    if t.dtype is not torch.int32:
-        raise TypeError(f"block_table must be int32 (got {t.dtype})")
-    shape = t.shape
-    if len(shape) != 2 or shape[0] < rows or shape[1] < 1:
-        raise ValueError(f"block_table must be 2-D with at least {rows} rows and a column (got {tuple(shape)})")
-    cols = shape[1]
-    ld, unit = t.stride()
-    if cols > 1 and unit != 1:
-        raise ValueError("block_table must have unit column stride")
-    if shape[0] == 1:
-        ld = max(ld, cols)
-    elif ld < cols:
-        raise ValueError(f"block_table: row stride {ld} is below its width {cols}")
-    return t.data_ptr(), ld, cols
+    try:
+        if t.dtype is not torch.int32:
+            raise TypeError(f"block_table must be an int32 torch tensor (got {t.dtype})")
+        shape = t.shape
+        if len(shape) != 2 or shape[0] < rows or shape[1] < 1:
+            raise ValueError(f"block_table must be 2-D with at least {rows} rows and a column (got {tuple(shape)})")
+        cols = shape[1]
+        ld, unit = t.stride()
+        if cols > 1 and unit != 1:
+            raise ValueError("block_table must have unit column stride")
+        if shape[0] == 1:
+            ld = max(ld, cols)
+        elif ld < cols:
+            raise ValueError(f"block_table: row stride {ld} is below its width {cols}")
+        return t.data_ptr(), ld, cols
+    except AttributeError:
+        raise TypeError("block_table must be a torch tensor") from None
 
 
 def _rows(t, dtype, rows: int, width: int, what: str) -> tuple:
     """(address, row stride) of a row-major [rows, width] matrix."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a torch tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{what} must be {dtype} (got {t.dtype})")
-    if t.shape != (rows, width):
-        raise ValueError(f"{what} must have shape ({rows}, {width}) (got {tuple(t.shape)})")
-    ld, unit = t.stride()
-    if unit != 1 and width > 1:
-        raise ValueError(f"{what} must have unit column stride (got stride {t.stride()})")
-    if rows <= 1:
-        ld = -(-max(ld, width) // 8) * 8   # the stride of a single row is never used
-    elif ld < width:
-        raise ValueError(f"{what}: row stride {ld} is below its width {width}")
-    return t.data_ptr(), ld
+    try:
+        if t.dtype is not dtype:
+            raise TypeError(f"{what} must be a torch tensor of {dtype} (got {t.dtype})")
+        if t.shape != (rows, width):
+            raise ValueError(f"{what} must have shape ({rows}, {width}) (got {tuple(t.shape)})")
+        ld, unit = t.stride()
+        if unit != 1 and width > 1:
+            raise ValueError(f"{what} must have unit column stride (got stride {t.stride()})")
+        if rows <= 1:
+            ld = -(-max(ld, width) // 8) * 8   # the stride of a single row is never used
+        elif ld < width:
+            raise ValueError(f"{what}: row stride {ld} is below its width {width}")
+        return t.data_ptr(), ld
+    except AttributeError:
+        raise TypeError(f"{what} must be a torch tensor") from None
 
 
 class KVCache:
