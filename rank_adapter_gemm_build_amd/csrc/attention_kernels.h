@@ -47,7 +47,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kJoin = 8;        // parts of a unit that one workgroup adds
-constexpr int kWholeLog2 = 2;   // units of so many steps are not cut while there are workgroups for all
 
 // Read-only words at a wave-uniform index through the scalar cache (written by earlier
 // launches only).
@@ -231,10 +230,12 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
   // ---- the line: steps before each sequence, and its shares
   const int per = (a.num_seqs + kThreads - 1) / kThreads;
   const int r0 = min(a.num_seqs, tid * per), r1 = min(a.num_seqs, r0 + per);
+  constexpr int kWholeLog2 = W == 1 ? 5 : 2;
   // Two lines: in steps, and in steps 2^kWholeLog2 times as long, of which every unit has one
   // if no sequence is longer.  The second is taken if that holds and the units fill a quarter
   // of the workgroups and no more than all: 64 sequences of 100 to 500 tokens, 8 heads, 24.9 us
-  // uncut, 29.2 cut; with 8 sequences 13.4, 11.9; with one 12.6, 11.3.
+  // uncut, 29.2 cut; with 8 sequences 13.4, 11.9; with one 12.6, 11.3.  One-wave workgroups:
+  // 256 sequences of 100 to 500 tokens 71.0 us uncut, 79.7 cut.
   int mine = 0, mine_whole = 0;
   bool long_one = false;
   int* whole_sums = sums + a.num_seqs;

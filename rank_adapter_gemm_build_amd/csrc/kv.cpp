@@ -406,11 +406,11 @@ lora_status lora_paged_attention(const lora_attention* attention, const void* q,
   const rax::AttnRows rows = rax::attention_rows(mean_rows, (long long)num_seqs * attention->kv_heads);
   a.row_tiles = rows.tiles;
   a.row_waves = rows.waves;
-  // One wave a workgroup where there is a unit for most of the waves and the table's width
-  // bounds their keys: 256 sequences of 8 to 60 tokens took 22.1 us against 29.1, of 100 to
-  // 500 79.0 against 80.1; of 2000 to 4000, where the table is wider, 590 against 536.
+  // One wave a workgroup where there is a unit for half of the waves and the table's width
+  // bounds their keys: 256 sequences of 16 to 128 tokens took 26.2 us against 33.7, of 100 to
+  // 500 70.4 against 77.8; of 400 to 990 153.9 against 142.7 with 4 waves.
   a.waves = rows.rows() == 16 && (long long)num_seqs * attention->kv_heads >= 2 * attention->workers &&
-            (long long)max_pages * cache->page_size <= 1024 ? 1 : 4;
+            (long long)max_pages * cache->page_size <= 640 ? 1 : 4;
   // two workgroups a compute unit fit in registers, above 128 dims one
   a.workers = attention->workers * (4 / a.waves) / (attention->dim > 128 ? 2 : 1);
   a.step_log2 = rax::attention_step_log2(a);
