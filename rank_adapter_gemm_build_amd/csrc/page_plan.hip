@@ -24,13 +24,17 @@ namespace rax {
 constexpr int kPlanThreads = 512, kPlanWaves = kPlanThreads / 64, kPlanPer = LORA_MAX_SEQS / kPlanThreads;
 constexpr int kPlanBatch = 4;   // elements of a thread whose loads are on the way together
 
-__device__ __forceinline__ int wave_sat_scan(int x) {   // inclusive
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
-    if (lane_id() >= d) x = sat_add(x, y);
-  }
-  return x;
+// inclusive, with all lanes active: wave_inclusive_scan's lane moves with the capped sum
+template <int CTRL, int ROWS> __device__ __forceinline__ int sat_step(int x) {
+  return sat_add(x, __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ int wave_sat_scan(int x) {
+  x = sat_step<0x111, 0xf>(x);   // row_shr:1
+  x = sat_step<0x112, 0xf>(x);   // row_shr:2
+  x = sat_step<0x114, 0xf>(x);   // row_shr:4
+  x = sat_step<0x118, 0xf>(x);   // row_shr:8
+  x = sat_step<0x142, 0xa>(x);   // row_bcast:15, rows 1 and 3
+  return sat_step<0x143, 0xc>(x);   // row_bcast:31, rows 2 and 3
 }
 
 // last r in [0, n) with start[r] <= x (start[0] = 0)
