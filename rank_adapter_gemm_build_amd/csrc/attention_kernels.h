@@ -70,6 +70,7 @@ __device__ __forceinline__ int here_lane(int v) {
 // offset is kNowhere, or a group whose descriptor is empty (a page outside the cache, a
 // tile past the last), reads zeros without a memory access or a branch.
 constexpr uint32_t kNowhere = 0x80000000u;
+constexpr int kStreaming = 2;   // buffer access bit nt
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t cells_at(const char* base, bool ok) {
@@ -78,16 +79,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t cells_at(const char* base, boo
 template <int N> struct Words {
   uint32_t w[N];
 };
-template <int N> __device__ __forceinline__ Words<N> load_words(__amdgpu_buffer_rsrc_t r, uint32_t ofs, uint32_t sofs) {
+template <int N, int AUX = 0> __device__ __forceinline__ Words<N> load_words(__amdgpu_buffer_rsrc_t r, uint32_t ofs, uint32_t sofs) {
   Words<N> x;
   if constexpr (N == 4) {
-    const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, ofs, sofs, 0);
+    const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, ofs, sofs, AUX);
     x.w[0] = v[0]; x.w[1] = v[1]; x.w[2] = v[2]; x.w[3] = v[3];
   } else if constexpr (N == 2) {
-    const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(r, ofs, sofs, 0);
+    const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(r, ofs, sofs, AUX);
     x.w[0] = v[0]; x.w[1] = v[1];
   } else {
-    x.w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, ofs, sofs, 0);
+    x.w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, ofs, sofs, AUX);
   }
   return x;
 }
@@ -207,8 +208,9 @@ struct Part {
   int s0, s1, steps, at;  // steps [s0, s1) of the unit's, and its place on the line
 };
 
-// RT: row tiles of a wave; W: waves; RW: those that share rows side by side
-template <typename C, int DB, int RT, int W, int RW>
+// RT: row tiles of a wave; W: waves; RW: those that have rows side by side; ONCE: every line of
+// the cache is read by one workgroup only, and passes the caches as a stream
+template <typename C, int DB, int RT, int W, int RW, bool ONCE>
 __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kernel(AttentionArgs a) {
   using S = AttnTile<C, DB>;
   using T = std::conditional_t<S::kF32, float, uint16_t>;
@@ -217,6 +219,7 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
   using JoinRows = float[16][S::kPitch];
   __shared__ int part_s[W][3], last_s;
 
+  constexpr int kAux = ONCE ? kStreaming : 0;
   constexpr int kThreads = 64 * W, KW = W / RW;   // KW: waves that split the keys
   constexpr int kRowsLog2 = 4 + RT / 2 + RW / 2, kRows = 1 << kRowsLog2, kKeysLog2 = S::kF32 ? 4 : 5;
   const int tid = threadIdx.x, lane = lane_id(), w = W == 1 ? 0 : uniform(tid >> 6), rw = w % RW, kw = w / RW;
@@ -506,14 +509,14 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
       for (int i = 0; i < G; ++i)
 #pragma unroll
         for (int f = 0; f < NK; ++f)
-          K[i][f] = __builtin_bit_cast(uint4, load_words<4>(cells_at(kbase + y.at[i], y.ok[i]), kofs[f], 0));
+          K[i][f] = __builtin_bit_cast(uint4, load_words<4, kAux>(cells_at(kbase + y.at[i], y.ok[i]), kofs[f], 0));
     };
     auto load_v = [&](const Place& y) {
 #pragma unroll
       for (int i = 0; i < 4 * G; ++i)
 #pragma unroll
         for (int vb = 0; vb < VB; ++vb)
-          V[vb][i] = load_words<VW>(cells_at(vbase + y.at[i / 4], y.ok[i / 4]), vofs[vb], (uint32_t)(i % 4) * tok_b);
+          V[vb][i] = load_words<VW, kAux>(cells_at(vbase + y.at[i / 4], y.ok[i / 4]), vofs[vb], (uint32_t)(i % 4) * tok_b);
     };
     int page[G];
     Place cur{}, nxt{};
@@ -799,22 +802,27 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
   }
 }
 
-template <typename C, int DB, int RT, int W, int RW>
+template <typename C, int DB, int RT, int W, int RW, bool ONCE>
 static void launch_shape(const AttentionArgs& a, hipStream_t stream, const KTimer& tm) {
   const uint32_t join = W > RW ? W * 16 * (AttnTile<C, DB>::kPitch + 2 * RT) : 2 * 16 * RT * RW;
-  RAX_LAUNCH(tm, (paged_attention_kernel<C, DB, RT, W, RW>), dim3(a.workers), dim3(64 * W),
+  RAX_LAUNCH(tm, (paged_attention_kernel<C, DB, RT, W, RW, ONCE>), dim3(a.workers), dim3(64 * W),
              (uint32_t)sizeof(float) * (join + 2 * a.num_seqs), stream, a);
 }
-template <typename C, int DB> static void launch_rows(const AttentionArgs& a, hipStream_t stream, const KTimer& tm) {
-  if (a.waves == 1) launch_shape<C, DB, 1, 1, 1>(a, stream, tm);
-  else if (a.row_tiles == 1) launch_shape<C, DB, 1, 4, 1>(a, stream, tm);
-  else if (a.row_waves == 1) launch_shape<C, DB, 2, 4, 1>(a, stream, tm);
-  else launch_shape<C, DB, 2, 4, 2>(a, stream, tm);
+template <typename C, int DB, bool ONCE>
+static void launch_rows(const AttentionArgs& a, hipStream_t stream, const KTimer& tm) {
+  if (a.waves == 1) launch_shape<C, DB, 1, 1, 1, ONCE>(a, stream, tm);
+  else if (a.row_tiles == 1) launch_shape<C, DB, 1, 4, 1, ONCE>(a, stream, tm);
+  else launch_shape<C, DB, 2, 4, 1, ONCE>(a, stream, tm);
+}
+template <typename C, int DB> static void launch_reads(const AttentionArgs& a, hipStream_t stream, const KTimer& tm) {
+  if (a.row_waves == 2) launch_shape<C, DB, 2, 4, 2, false>(a, stream, tm);
+  else if (a.read_once) launch_rows<C, DB, true>(a, stream, tm);
+  else launch_rows<C, DB, false>(a, stream, tm);
 }
 template <typename C> hipError_t launch_attention_of(const AttentionArgs& a, hipStream_t stream, const KTimer& tm) {
-  if (a.c.dim <= 64) launch_rows<C, 64>(a, stream, tm);
-  else if (a.c.dim <= 128) launch_rows<C, 128>(a, stream, tm);
-  else launch_rows<C, 256>(a, stream, tm);
+  if (a.c.dim <= 64) launch_reads<C, 64>(a, stream, tm);
+  else if (a.c.dim <= 128) launch_reads<C, 128>(a, stream, tm);
+  else launch_reads<C, 256>(a, stream, tm);
   return hipGetLastError();
 }
 

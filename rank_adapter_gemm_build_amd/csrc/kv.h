@@ -48,6 +48,7 @@ struct AttentionArgs {
   float scale;
   // the launch's shape and workspace
   int waves, row_tiles, row_waves;   // of a workgroup; its rows: 16 * row_tiles * row_waves
+  int read_once;                     // no line of the cache is read by two workgroups
   int workers, min_steps;            // workgroups; steps each has at least
   int step_log2;                     // keys of a step
   int group_size;                    // query heads of a kv head
