@@ -7,8 +7,9 @@
 // sequence); the work on each is done by the matrix cores in a small part of that time.
 //
 // Rows.  The new tokens of a sequence times the query heads of one kv head share its keys:
-// row x = token * group + head.  A wave holds RT tiles of 16 rows; a workgroup of 4 waves
-// has row_waves row groups, the other waves split the keys (KW = 4 / row_waves).
+// row x = token * group + head.  A wave holds RT tiles of 16 rows; of a workgroup's W waves
+// RW have rows side by side, the others split the keys (KW = W / RW).  A workgroup of one wave
+// (many short sequences) needs no join and no LDS.
 //
 // Tiles.  Both products keep the rows in the matrix cores' column (lane % 16), so maxima,
 // sums and the correction of o stay in the lane they are used in, and nothing passes
@@ -16,7 +17,7 @@
 //   S^T = K Q^T: lane (c, g = lane / 16) gets row c's scores of keys 4 g + 0..3 of each
 //   group of 16 keys; these are exactly its operand values of O^T = V^T P^T when the second product's
 //   contraction index 8 g + i stands for key 4 g + i of the first (i < 4) or second group.
-//   K is the operand as it lies in memory (a lane loads 16 bytes of one key).  V needs
+//   K is the operand as it lies in memory (a lane loads 16 bytes of one key; whole_keys). V needs
 //   several keys of one dim in a register: a lane loads EC consecutive dims of each of its
 //   keys and the pairs are put together by one byte permutation each.  MFMA e of a block
 //   then computes the dims {m EC + e}, so a lane ends with EC consecutive dims of its row.
@@ -24,13 +25,19 @@
 //   second product is far from binding.  e4m3 cells are widened to bf16, which is exact.
 //   fp32 caches use the fp32 matrix cores, 4 keys (or dims) at a time, with no permutation.
 // A tile's keys are loaded again as soon as its first product has read them, its values
-// after the second, so every wave keeps 8 to 16 KB on the way.
+// after the second, so every wave keeps 8 to 16 KB on the way, and a part's first tile is
+// loaded before the part before it is joined and written.
 //
 // Split.  The steps (KW tiles) of all sequences, kv heads and row blocks form one
 // line, cut into equal contiguous shares, one a workgroup, whatever the lengths.  What a
 // workgroup has of a unit (sequence, head, row block) that others share goes to the
-// workspace as (m, l, o); the last one to arrive adds the parts in order of the keys, so
-// the result does not depend on which that is.
+// workspace as (m, l, o); the parts join in a tree, the last one to arrive at a node adding
+// them in order of the keys, so the result does not depend on which that is.
+//
+// Measured: 256 sequences of 2000 to 4000 tokens, 32 query and 8 kv heads of 128, bf16:
+// 482 to 498 us, 6.3 to 6.5 TB/s (a plain streaming read reaches 6.15, a copy 5.3); one of
+// 131071 88 us, 6.1 TB/s; one of 777 11 us, latency: 2 us launch, 1 the line, 1 the part, 2.5 page
+// ids and first tile, 4.5 join.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -91,6 +98,24 @@ template <int N, int AUX = 0> __device__ __forceinline__ Words<N> load_words(__a
     x.w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, ofs, sofs, AUX);
   }
   return x;
+}
+
+// A pair of loads covers 128 bytes of each of 16 keys.  Each load takes whole lines, of 8 keys
+// (streamed lines that two loads touch cost more: 64 sequences to 8192, e4m3 rows of 128
+// bytes, 118 -> 108 us, bf16 to 4096 106.5 -> 102.3; rows that follow each other in memory
+// within 2 % either way; 256-byte pieces of 4 keys no better): lane c16 of `a` holds key c16 % 8, of `b` 8 + c16 % 8, bytes 64 (c16 / 8)
+// on.  The matrix cores' operands have key c16 in lane c16, the first 64 bytes in one and the
+// others in the next, so the lanes of a row of 16 exchange with those 8 away.
+__device__ __forceinline__ void whole_keys(uint4& a, uint4& b) {
+  const auto step = [](uint32_t& u, uint32_t& v) {
+    const int x = (int)u, y = (int)v;
+    u = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xf, 0xc, false);   // row_ror:8 into lanes 8..15
+    v = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xf, 0x3, false);   // into lanes 0..7
+  };
+  step(a.x, b.x);
+  step(a.y, b.y);
+  step(a.z, b.z);
+  step(a.w, b.w);
 }
 
 // What workgroups hand to each other inside a launch goes past the caches that the XCDs do
@@ -214,7 +239,7 @@ template <typename C, int DB, int RT, int W, int RW, bool ONCE>
 __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kernel(AttentionArgs a) {
   using S = AttnTile<C, DB>;
   using T = std::conditional_t<S::kF32, float, uint16_t>;
-  constexpr int G = S::kGroups, NK = S::kKLoads, NQ = S::kQFrags, EC = S::kEC, VB = S::kVB, VW = S::kVW;
+  constexpr int G = S::kGroups, NK = S::kKLoads, NP = NK > 1 ? NK / 2 : 1, NQ = S::kQFrags, EC = S::kEC, VB = S::kVB, VW = S::kVW;
   extern __shared__ float4 lds[];
   using JoinRows = float[16][S::kPitch];
   __shared__ int part_s[W][3], last_s;
@@ -285,10 +310,12 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
 
   const uint32_t tok_b = (uint32_t)a.c.token_stride * (uint32_t)sizeof(C);   // below 2^27
   const float qs = a.scale * a.c.k_scale * 1.44269504088896341f;
-  uint32_t kofs[NK], vofs[VB];   // lane's place in a group of keys, of values
+  uint32_t kofs[NP], vofs[VB];   // lane's place in a group of keys, of values
 #pragma unroll
-  for (int f = 0; f < NK; ++f)
-    kofs[f] = f * S::kKElems * 4 + g4 * S::kKElems < D ? (uint32_t)c16 * tok_b + 16u * g4 + 64u * f : kNowhere;
+  for (int f = 0; f < NP; ++f) {
+    const uint32_t at = (NK > 1 ? 128u * f + 64u * (c16 >> 3) : 0u) + 16u * g4;   // in the key's row
+    kofs[f] = at < (uint32_t)D * (uint32_t)sizeof(C) ? (uint32_t)(NK > 1 ? c16 & 7 : c16) * tok_b + at : kNowhere;
+  }
 #pragma unroll
   for (int vb = 0; vb < VB; ++vb) {
     const int d = (vb * 16 + c16) * EC;
@@ -509,7 +536,7 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
       for (int i = 0; i < G; ++i)
 #pragma unroll
         for (int f = 0; f < NK; ++f)
-          K[i][f] = __builtin_bit_cast(uint4, load_words<4, kAux>(cells_at(kbase + y.at[i], y.ok[i]), kofs[f], 0));
+          K[i][f] = __builtin_bit_cast(uint4, load_words<4, kAux>(cells_at(kbase + y.at[i], y.ok[i]), kofs[NK > 1 ? f / 2 : f], f % 2 * 8 * tok_b));
     };
     auto load_v = [&](const Place& y) {
 #pragma unroll
@@ -607,6 +634,12 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
       const unsigned key0 = base + t * S::kKeys;
       nxt = place_of(t + KW, page);
       page_of(t + 2 * KW, page);
+      if constexpr (NK > 1) {
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+          for (int f = 0; f < NK; f += 2) whole_keys(K[i][f], K[i][f + 1]);
+      }
       // scores
       f32x4_t sc[RT][G];
 #pragma unroll
