@@ -552,8 +552,9 @@ lora_status lora_rotary_append(const lora_rotary* rotary, const void* qkv, int l
 /*
  * Attention of a step's tokens over the paged cache.  The object owns the workspace for
  * max_seqs sequences and max_tokens new tokens of num_q_heads query and num_kv_heads key/value
- * heads: partial results of long sequences, which several workgroups share, and the
- * counters that tell the last of them to join.
+ * heads: partial results of long sequences, which several workgroups share (256 KiB a head_dim
+ * value on 256 compute units, 32 MiB at 128, whatever the other sizes), and the counters
+ * that tell the last of them to join.
  * Errors of create: out NULL -> INVALID_ARG; max_seqs outside [1, LORA_MAX_SEQS],
  * max_tokens outside [1, 2^24] or, times num_q_heads / num_kv_heads, above 2^30, num_kv_heads outside
  * [1, 1024], num_q_heads not a multiple of it or above 1024, head_dim above

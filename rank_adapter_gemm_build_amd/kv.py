@@ -178,7 +178,8 @@ def page_plan(plan: PagePlan, past_lens, new_lens, num_tokens: int, free_pages, 
     lora_page_plan).  past_lens, new_lens: int32 [requests]; num_tokens: entries of
     plan.positions and plan.slots to fill (the batch's tokens, or more for a padded step);
     free_pages: int32 ring [num_pages]; cursor: int32 [4] (first free place, free pages, 0,
-    0); cursor_out: where the advanced cursor goes (default: cursor itself)."""
+    0); cursor_out: where the advanced cursor goes (default: cursor itself).  Nothing the call
+    writes may overlap its other vectors: past_lens is not plan.seq_lens, but a copy of it."""
     if torch is None:
         _load()
     dev = plan.device
