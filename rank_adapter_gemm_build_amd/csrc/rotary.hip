@@ -62,9 +62,12 @@ enum RotaryPairs { kInterleaved, kHalves, kOddHalves };
 template <typename T, typename C, int PAIRS>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_append_kernel(RotaryArgs a) {
   constexpr int V = 16 / (int)sizeof(T);   // values of a chunk
-  __shared__ float2 turn[kRotaryTokens * LORA_MAX_HEAD_DIM / 2];   // cos, sin of [token][pair]
+  // a slice of heads (kOddHalves), then cos, sin of [token][pair]: no more than the launch's
+  // tokens need, for as many workgroups a compute unit as registers allow
+  extern __shared__ uint4 lds[];
   __shared__ int slot_s[kRotaryTokens];
-  __shared__ uint4 slice[PAIRS == kOddHalves ? kRotarySlice / 16 : 1];
+  uint4* slice = lds;
+  float2* turn = reinterpret_cast<float2*>(lds + (PAIRS == kOddHalves ? kRotarySlice / 16 : 0));
   const int tid = threadIdx.x, D = a.c.dim, half = a.rot / 2, turned = a.q_heads + a.c.heads;
   const int t0 = blockIdx.x * a.tokens_wg, tokens = min(a.tokens_wg, a.num_tokens - t0);
 
@@ -216,12 +219,13 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_append_kernel(RotaryArg
 template <int PAIRS>
 static void launch_pairs(const RotaryArgs& a, const dim3& grid, hipStream_t stream, const KTimer& tm) {
   const dim3 block(kRotaryThreads);
+  const uint32_t lds = (uint32_t)((PAIRS == kOddHalves ? kRotarySlice : 0) + a.tokens_wg * (a.rot / 2) * (int)sizeof(float2));
   if (a.dtype == LORA_F32)
-    RAX_LAUNCH(tm, (rotary_append_kernel<float, float, PAIRS>), grid, block, 0u, stream, a);
+    RAX_LAUNCH(tm, (rotary_append_kernel<float, float, PAIRS>), grid, block, lds, stream, a);
   else if (a.c.dtype == LORA_FP8E4M3)
-    RAX_LAUNCH(tm, (rotary_append_kernel<uint16_t, uint8_t, PAIRS>), grid, block, 0u, stream, a);
+    RAX_LAUNCH(tm, (rotary_append_kernel<uint16_t, uint8_t, PAIRS>), grid, block, lds, stream, a);
   else
-    RAX_LAUNCH(tm, (rotary_append_kernel<uint16_t, uint16_t, PAIRS>), grid, block, 0u, stream, a);
+    RAX_LAUNCH(tm, (rotary_append_kernel<uint16_t, uint16_t, PAIRS>), grid, block, lds, stream, a);
 }
 
 hipError_t launch_rotary_append(const RotaryArgs& args, hipStream_t stream, const KTimer& tm) {
