@@ -580,10 +580,12 @@ lora_status lora_attention_destroy(lora_attention* attention);
  * with one rounding to out.  The result is bitwise the same on every call.  Rows of no sequence are left as
  * they were; seq_lens outside [0, max_pages * page_size] are taken as the nearer bound,
  * query_start outside [0, num_tokens] likewise; a sequence that ends before it starts has
- * no tokens.  One launch on `stream`.  Two calls on one object must not overlap in time.
+ * no tokens (starts that overlap so much that the work passes 2^30 steps: nothing is
+ * written).  One launch on `stream`.  Two calls on one object must not overlap in time.
  * Errors: INVALID_ARG (NULL pointer, scale not finite, window < 0), SHAPE (heads or
  * head_dim not the object's, ld_table < max_pages, strides below the rows' width,
- * max_pages < 1, the cache's rules), CAPACITY (num_seqs or num_tokens above the object's), DTYPE, ALIGN.
+ * max_pages < 1, the cache's rules, num_tokens * num_q_heads of 2^30 and more that need 2^30
+ * steps), CAPACITY (num_seqs or num_tokens above the object's), DTYPE, ALIGN.
  */
 lora_status lora_paged_attention(const lora_attention* attention, const void* q, int ldq, lora_dtype dtype,
                                  const lora_kv_cache* cache, const int32_t* block_table, int ld_table, int max_pages,

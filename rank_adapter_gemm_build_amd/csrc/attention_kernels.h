@@ -47,6 +47,7 @@
 
 #include "device_util.h"
 #include "kv.h"
+#include "kv_scan.h"
 
 namespace rax {
 
@@ -272,11 +273,12 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
     const int units = a.c.heads * row_blocks(s.n, group, kRowsLog2), steps = seq_span(s, a.window, a.step_log2).steps;
     sums[i] = mine;
     whole_sums[i] = mine_whole;
-    mine += units * steps;
-    mine_whole += units;
+    const long long all = (long long)units * steps;
+    mine = sat_add(mine, all < kPlanCap ? (int)all : kPlanCap);
+    mine_whole = sat_add(mine_whole, units);
     long_one |= steps > (1 << kWholeLog2);
   }
-  const int scan = wave_inclusive_scan(mine), scan_whole = wave_inclusive_scan(mine_whole);
+  const int scan = wave_sat_scan(mine), scan_whole = wave_sat_scan(mine_whole);
   long_one = __any(long_one);
   if (lane == 63) {
     part_s[w][0] = scan;
@@ -291,13 +293,14 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
       before += part_s[v][0];
       units_before += part_s[v][1];
     }
-    work_ += part_s[v][0];
-    units += part_s[v][1];
+    work_ = sat_add(work_, part_s[v][0]);
+    units = sat_add(units, part_s[v][1]);
     long_one |= part_s[v][2] != 0;
   }
-  const bool by_unit = uniform(!long_one && units <= (int)gridDim.x && units >= (int)gridDim.x / 4) != 0;
+  const bool by_unit = uniform(!long_one && a.step_log2 + kWholeLog2 < 31 && units <= (int)gridDim.x && units >= (int)gridDim.x / 4) != 0;
   work_ = uniform(by_unit ? units : work_);
-  if (work_ == 0) return;
+  // no work, or more than the host counted with: sequences that overlap (the sums are capped)
+  if (work_ == 0 || work_ >= kPlanCap) return;
   for (int i = r0; i < r1; ++i) sums[i] = by_unit ? whole_sums[i] + units_before : sums[i] + before;
   const int step_log2 = a.step_log2 + (by_unit ? kWholeLog2 : 0), tiles_log2 = step_log2 - kKeysLog2;   // tiles of a step
   const int workers_ = by_unit ? work_ : min((work_ + a.min_steps - 1) / a.min_steps, (int)gridDim.x);

@@ -425,6 +425,8 @@ lora_status lora_paged_attention(const lora_attention* attention, const void* q,
   a.min_steps = a.waves == 1 ? 1 : std::max(1, std::max(128, 4 * rows.rows()) >> a.step_log2);
   a.step_log2 = rax::line_step_log2(a.step_log2, num_seqs, num_tokens, max_pages * cache->page_size, attention->kv_heads,
                                     a.group_size, log2_of(rows.rows()));
+  if (a.step_log2 < 0)
+    return fail(LORA_ERR_SHAPE, "num_tokens %d times %d query heads is too much for one call", num_tokens, attention->q_heads);
   a.part_o = attention->part_o;
   a.part_ml = attention->part_ml;
   a.arrived = attention->arrived;

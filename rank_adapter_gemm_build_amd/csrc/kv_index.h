@@ -115,14 +115,13 @@ RAX_HD SeqSpan seq_span(const SeqRows& s, int window, int step_log2) {
 RAX_HD int row_blocks(int n, int group, int rows_log2) {
   return (int)(((unsigned)n * (unsigned)group + ((1u << rows_log2) - 1u)) >> rows_log2);   // n * group <= 2^30
 }
-// The least step_log2 >= least with which the line of all units' steps is below 2^31
-// whatever the lengths on the device are (no more than max_len keys and num_tokens tokens
-// a sequence).
+// The least step_log2 >= least with which the line of all units' steps is below kPlanCap for
+// sequences of up to max_len keys that share num_tokens tokens; -1 if there is none up to 30.
 RAX_HD int line_step_log2(int least, int num_seqs, int num_tokens, int max_len, int heads, int group, int rows_log2) {
-  const double units = (double)num_seqs * heads * row_blocks(num_tokens, group, rows_log2);
+  const double units = ((double)row_blocks(num_tokens, group, rows_log2) + num_seqs) * heads;
   int s = least;
-  while (s < 31 && units * ((double)(max_len >> s) + 2.0) >= 2147483648.0) ++s;
-  return s;
+  while (s <= 30 && units * ((double)(max_len >> s) + 2.0) >= kPlanCap) ++s;
+  return s <= 30 ? s : -1;
 }
 
 // Contiguous equal shares of `work` steps: worker b of g takes [share_start(b), share_start(b + 1)).

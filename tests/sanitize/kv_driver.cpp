@@ -306,13 +306,22 @@ static void share_walk() {
                   1 << 30, INT_MAX, INT_MAX / d * d - 1, INT_MAX / d * d})
       TRUE(rax::fast_quot(n, f) == n / d);
   }
-  for (int i = 0; i < 3000; ++i) {   // the line fits 31 bits, also with every sequence at its bounds
-    const int seqs = 1 + g() % LORA_MAX_SEQS, group = 1 + g() % 1024, heads = 1 + g() % 1024, rows_log2 = 4 + g() % 4;
-    const int T = 1 + (int)(g() % std::min(1 << 24, (1 << 30) / group)), max_len = 1 + (int)(g() % INT_MAX);
+  for (int i = 0; i < 3000; ++i) {   // the line stays below the cap, also with every key and token there is
+    const int seqs = 1 + g() % LORA_MAX_SEQS, group = 1 + g() % 64, heads = 1 + g() % (1024 / group), rows_log2 = 4 + g() % 3;
+    const int T = 1 + (int)(g() % (g() % 2 ? 70000 : 1 << 24)), max_len = 1 + (int)(g() % (g() % 2 ? 1 << 20 : INT_MAX));
     const int step = rax::line_step_log2(5, seqs, T, max_len, heads, group, rows_log2);
-    if ((double)seqs * heads * rax::row_blocks(T, group, rows_log2) * 2.0 >= 2147483648.0) continue;   // step 31: refused
-    const rax::SeqSpan x = rax::seq_span(rax::SeqRows{0, T, max_len}, 0, step);
-    TRUE((double)x.steps * seqs * heads * rax::row_blocks(T, group, rows_log2) < 2147483648.0);
+    TRUE(step == -1 || (step >= 5 && step <= 30));
+    if (step < 0) {   // refused: there are that many units
+      TRUE(((double)rax::row_blocks(T, group, rows_log2) + seqs) * heads * 4.0 >= rax::kPlanCap);
+      continue;
+    }
+    double line = 0;
+    for (int r = 0; r < seqs; ++r) {   // tokens dealt evenly, all sequences of the longest length
+      const int n = T / seqs + (r < T % seqs);
+      const rax::SeqSpan x = rax::seq_span(rax::SeqRows{0, n, max_len}, 0, step);
+      line += (double)x.steps * heads * rax::row_blocks(n, group, rows_log2);
+    }
+    TRUE(line < rax::kPlanCap);
   }
   for (long long rows : {1LL, 16LL, 17LL, 33LL, 65LL, 1LL << 30})
     for (long long heads : {1LL, 64LL, 128LL, 4096LL * 1024}) {
