@@ -400,34 +400,34 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
             }
         }
       } else {
-      constexpr int kTileRows = 16 * RT * (RW - 1) + 16;   // local rows of this row tile lie below
+        constexpr int kTileRows = 16 * RT * (RW - 1) + 16;   // local rows of this row tile lie below
 #pragma unroll
-      for (int vb = 0; vb < VB; ++vb) {
-        if (rt + vb > 0) lds_barrier();
+        for (int vb = 0; vb < VB; ++vb) {
+          if (rt + vb > 0) lds_barrier();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float* d = &buf[w][c16][(4 * g4 + k) * EC];
+          for (int k = 0; k < 4; ++k) {
+            float* d = &buf[w][c16][(4 * g4 + k) * EC];
 #pragma unroll
-          for (int e = 0; e < EC; e += 4)
-            *reinterpret_cast<f32x4_t*>(d + e) = f32x4_t{o[rt][vb * EC + e][k] * f, o[rt][vb * EC + e + 1][k] * f,
-                                                        o[rt][vb * EC + e + 2][k] * f, o[rt][vb * EC + e + 3][k] * f};
+            for (int e = 0; e < EC; e += 4)
+              *reinterpret_cast<f32x4_t*>(d + e) = f32x4_t{o[rt][vb * EC + e][k] * f, o[rt][vb * EC + e + 1][k] * f,
+                                                          o[rt][vb * EC + e + 2][k] * f, o[rt][vb * EC + e + 3][k] * f};
+          }
+          lds_barrier();
+          constexpr int kChunks = 4 * EC;   // of 4 dims
+          const int n = min(p.rows - rt * 16, kTileRows);
+          for (int it = tid; it < n * kChunks; it += kThreads) {
+            const int d4 = it % kChunks, y = it / kChunks, rv = y / (16 * RT), row16 = y - rv * 16 * RT;   // y: local row - 16 rt
+            const int d = vb * 16 * EC + d4 * 4, row = rt * 16 + y;
+            if (row16 >= 16 || d >= D) continue;
+            f32x4_t v[KW], acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < KW; ++j) v[j] = *reinterpret_cast<const f32x4_t*>(&buf[rv + j * RW][row16][d4 * 4]);
+#pragma unroll
+            for (int j = 0; j < KW; ++j) acc += v[j];
+            if (whole) write4(out_row(p, row).out + d, acc);
+            else put_shared(part_o, (part_row(b - first, row) * D + d) * 4, acc);
+          }
         }
-        lds_barrier();
-        constexpr int kChunks = 4 * EC;   // of 4 dims
-        const int n = min(p.rows - rt * 16, kTileRows);
-        for (int it = tid; it < n * kChunks; it += kThreads) {
-          const int d4 = it % kChunks, y = it / kChunks, rv = y / (16 * RT), row16 = y - rv * 16 * RT;   // y: local row - 16 rt
-          const int d = vb * 16 * EC + d4 * 4, row = rt * 16 + y;
-          if (row16 >= 16 || d >= D) continue;
-          f32x4_t v[KW], acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < KW; ++j) v[j] = *reinterpret_cast<const f32x4_t*>(&buf[rv + j * RW][row16][d4 * 4]);
-#pragma unroll
-          for (int j = 0; j < KW; ++j) acc += v[j];
-          if (whole) write4(out_row(p, row).out + d, acc);
-          else put_shared(part_o, (part_row(b - first, row) * D + d) * 4, acc);
-        }
-      }
       }
     }
     if (!whole) {
