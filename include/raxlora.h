@@ -573,7 +573,8 @@ lora_status lora_attention_destroy(lora_attention* attention);
  * window > 0 only j > P - window.  (The new tokens' own keys and values are in the cache:
  * lora_rotary_append.)  Query head h reads kv head h / (num_q_heads / num_heads).  lse[t][h]
  * (fp32, may be NULL) = ln sum_j exp(scale q . k_j).  A token that sees nothing (length
- * 0, absent pages) gets zeros and lse = -inf.  What lies in the cache at unseen places,
+ * 0, absent pages) gets zeros and lse = -inf, as does one whose every score is -inf; a NaN score
+ * makes its token's head NaN in out and lse.  What lies in the cache at unseen places,
  * infinities and NaN included, has no effect.
  * q, out: [num_tokens][num_q_heads * head_dim], row strides ldq and ldo, dtype as for
  * lora_rotary_append (out has q's dtype).  Sums, maxima and products accumulate in fp32,

@@ -209,11 +209,14 @@ __device__ __forceinline__ void write4(float* p, f32x4_t y) { *reinterpret_cast<
 __device__ __forceinline__ void write8(uint16_t* p, f32x4_t y, f32x4_t z) {
   st16(p, make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3])));
 }
-// l is 0 (nothing seen) or at least 1 / 2: the maximum's own weight is 1, and a part's join
-// keeps that
+// l is 0 (nothing seen, or scores of minus infinity only), NaN (a NaN score; the maximum
+// passes over it) or at least 1 / 2: the maximum's own weight is 1, and a part's join keeps that
 __device__ __forceinline__ float log_sum(float m, float l) {
-  return m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+  return l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
 }
+// The maximum that weights are taken relative to. A part without a finite score has the maximum
+// minus infinity and by that the weight 0 in a join; its sums, 0 or NaN, are added like all others.
+__device__ __forceinline__ float finite_top(float m) { return m == -INFINITY ? 0.f : m; }
 // scale / l, good to 2^-22
 __device__ __forceinline__ float over_sum(float scale, float l) { return scale * __builtin_amdgcn_rcpf(l); }
 
@@ -367,11 +370,10 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
         }
         sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < KW; ++j)
-          if (y[j].x != -INFINITY) sum += y[j].y * __builtin_amdgcn_exp2f(y[j].x - top);
-        f = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[rt] - top);
+        for (int j = 0; j < KW; ++j) sum += y[j].y * __builtin_amdgcn_exp2f(y[j].x - finite_top(top));
+        f = __builtin_amdgcn_exp2f(m[rt] - finite_top(top));
       }
-      if (whole) f = top == -INFINITY ? 0.f : f * over_sum(a.c.v_scale, sum);
+      if (whole) f = sum == 0.f ? 0.f : f * over_sum(a.c.v_scale, sum);
       if (kw == 0 && g4 == 0 && lrow < p.rows) {
         if (!whole) put_shared2(part_ml, part_row(b - first, lrow) * 8, top, sum);
         else if (a.lse) a.lse[out_row(p, lrow).lse] = log_sum(top, sum);
@@ -468,15 +470,14 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
             if (k < n) mm = fmaxf(mm, x[k].x);
 #pragma unroll
           for (int k = 0; k < kJoin; ++k)
-            if (k < n && x[k].x != -INFINITY) {
-              const float f = __builtin_amdgcn_exp2f(x[k].x - mm);
+            if (k < n) {
+              const float f = __builtin_amdgcn_exp2f(x[k].x - finite_top(mm));
               ll += x[k].y * f;
               acc += v[k] * f;
             }
           if (root) {
             const auto y = out_row(p, lrow);
-            const float f = mm == -INFINITY ? 0.f : over_sum(a.c.v_scale, ll);
-            write4(y.out + d, mm == -INFINITY ? f32x4_t{0.f, 0.f, 0.f, 0.f} : acc * f);
+            write4(y.out + d, acc * (ll == 0.f ? 0.f : over_sum(a.c.v_scale, ll)));
             if (a.lse && d == 0) a.lse[y.lse] = log_sum(mm, ll);
           } else {
             const uint32_t at = part_row(k0, lrow);
@@ -703,7 +704,7 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
 #pragma unroll
           for (int j = 0; j < VB * EC; ++j) o[rt][j] *= keep;
         }
-        const float mz = m[rt] == -INFINITY ? 0.f : m[rt];
+        const float mz = finite_top(m[rt]);
 #pragma unroll
         for (int i = 0; i < G; ++i)
 #pragma unroll
