@@ -1,7 +1,8 @@
 """One attention layer of a LoRA server over a paged cache, step by step as a server runs it.
 
 A prompt step (requests with prompts of different lengths), decode steps replayed from one
-captured graph, a step in which a request ends and another comes in its pages, each:
+captured graph, a step in which a request ends and another comes in its pages, steps with too
+few pages, whose last request is refused until pages have come back, each:
 
     page plan -> packed q/k/v projection + its LoRA correction -> rotary append ->
     paged attention -> o projection + its LoRA correction
@@ -19,8 +20,14 @@ import torch  # noqa: E402
 import rank_adapter_gemm_build_amd as rx  # noqa: E402
 
 HIDDEN, HEADS, KV_HEADS, DIM, PAGE, SLOTS, RANK, SCALE = 512, 8, 2, 64, 16, 3, 8, 0.5
-REQUESTS, MAX_LEN, PAGES, MAX_TOKENS = 4, 128, 40, 128
+REQUESTS, MAX_LEN, PAGES, MAX_TOKENS = 4, 128, 16, 128
 QKV = [HEADS * DIM, KV_HEADS * DIM, KV_HEADS * DIM]
+
+
+def advance(past, new, seq_lens):
+    """The cached lengths after a step, on the device: the plan gives length 0 to ended requests and to refused ones,
+    which keep what they have and ask again."""
+    past.copy_(torch.where(seq_lens > 0, seq_lens, torch.where(new < 0, 0, past)))
 
 
 class Layer:
@@ -88,7 +95,7 @@ def main(decode_steps: int = 6, seed: int = 0) -> float:
     past, new = torch.zeros(REQUESTS, **i32), torch.zeros(REQUESTS, **i32)
     slots_of = [0, 1, -1, 2]                      # the adapter of each request (-1: none)
     history = [torch.zeros(0, HIDDEN, dtype=torch.bfloat16, device="cuda") for _ in range(REQUESTS)]
-    worst = 0.0
+    worst, refusals = 0.0, 0
 
     def buffers(T):
         def rows(width):
@@ -99,11 +106,16 @@ def main(decode_steps: int = 6, seed: int = 0) -> float:
         return torch.tensor([s for s, n in zip(slots_of, counts) for _ in range(max(n, 0))], **i32)
 
     def check(x, y, counts):
-        nonlocal worst
-        torch.cuda.synchronize()
+        nonlocal worst, refusals
+        granted = plan.seq_lens[:REQUESTS].tolist()
+        refusals += plan.query()["refused"]
         at = 0
         for r, n in enumerate(counts):
             if n <= 0:
+                continue
+            if not granted[r]:                    # nothing of it was stored: its tokens come again
+                assert not y[at:at + n].any()
+                at += n
                 continue
             history[r] = torch.cat([history[r], x[at:at + n]])
             want = layer.dense(history[r], slots_of[r])[-n:]
@@ -119,7 +131,7 @@ def main(decode_steps: int = 6, seed: int = 0) -> float:
         rx.page_plan(plan, past, new, T, ring, cursor, layer.table, PAGE)
         layer.step(plan, x, ids_of(counts), qkv, q, attended, y)
         check(x, y, counts)
-        past.copy_(plan.seq_lens[:REQUESTS])      # the plan reads past while it writes seq_lens
+        advance(past, new, plan.seq_lens[:REQUESTS])
 
     eager_step([37, 16, 1, 50])                   # prompts
     # decode: one token a request, the whole step in a graph
@@ -130,7 +142,7 @@ def main(decode_steps: int = 6, seed: int = 0) -> float:
     def decode():
         rx.page_plan(plan, past, new, REQUESTS, ring, cursor, layer.table, PAGE)
         layer.step(plan, x, ids, qkv, q, attended, y)
-        past.copy_(plan.seq_lens[:REQUESTS])
+        advance(past, new, plan.seq_lens[:REQUESTS])
     layer.step(plan, x[:0], ids[:0], qkv[:0], q[:0], attended[:0], y[:0])   # library set-up stays out of the graph
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -149,8 +161,14 @@ def main(decode_steps: int = 6, seed: int = 0) -> float:
     # request 1 ends; its place goes to a new request in the step after, in pages that came back
     eager_step([1, -1, 1, 1])
     history[1], slots_of[1] = history[1][:0], 2
-    past[1] = 0
     eager_step([1, 33, 1, 2])
+    # too few pages for request 3, also in the step in which request 0's come back; then there are
+    eager_step([40, 30, 1, 40])
+    eager_step([-1, 1, 1, 40])
+    history[0] = history[0][:0]
+    assert refusals == 2, "request 3 was to be refused twice"
+    eager_step([16, 1, 1, 40])
+    assert refusals == 2, "request 3 was to get its pages"
     held = sum(-(-len(h) // PAGE) for h in history)
     assert plan.query()["free_pages"] == PAGES - held, "pages lost"
     print(f"paged serving ok: lengths {[len(h) for h in history]}, {plan.query()['free_pages']} of {PAGES} pages free, "

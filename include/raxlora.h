@@ -472,7 +472,9 @@ typedef struct lora_kv_cache {
  *   - An ended request's pages (those of its past tokens) go to the ring's end, in order
  *     of request and page; the step itself does not draw them.  Its row stays as it is.
  * Written: seq_lens[num_seqs] = past + new, or 0 for ended and refused requests (lora_paged_attention
- * then gives zeros); query_start[num_seqs + 1] = first token of each request; for t <
+ * then gives zeros; a refused request keeps its pages and asks again with the same past, so the next
+ * step's past is seq_lens only where that is above 0, else 0 after an end and the past before it
+ * otherwise); query_start[num_seqs + 1] = first token of each request; for t <
  * num_tokens positions[t] = past + index in the request and slots[t] (-1 for refused
  * requests); tokens past the batch's last get position 0 and slot -1, so a step of fixed size can be
  * padded.  cursor_out[0..1] = the ring after the step; cursor_out may be cursor (a step
