@@ -165,6 +165,8 @@ class PagePlan:
             return torch.zeros(max(1, n), dtype=torch.int32, device=f"cuda:{device}")
         self.seq_lens, self.query_start = vec(max_seqs), vec(max_seqs + 1)
         self.positions, self.slots, self.meta = vec(max_tokens), vec(max_tokens), vec(LORA_PLAN_META)
+        if not torch.cuda.is_current_stream_capturing():      # the vectors are ready for steps on any stream
+            torch.cuda.current_stream(device).synchronize()
         self._out = [t.data_ptr() for t in (self.seq_lens, self.query_start, self.positions, self.slots, self.meta)]
 
     def query(self) -> dict:
