@@ -538,7 +538,8 @@ lora_status lora_rotary_destroy(lora_rotary* rotary);
  * Rotary positions on a step's packed q/k/v rows, and the keys and values into the cache:
  * row t of qkv is [num_q_heads + 2 num_heads][head_dim] (q heads, k heads, v heads; row
  * stride ldqkv).  q_out[t] (row stride ldq) = the turned q heads, k[slot] = the turned k
- * heads, v[slot] = the v heads.  Angles are formed in 64 bits, the turn in fp32, one rounding
+ * heads, v[slot] = the v heads.  Angles are formed in 64 bits (good to 2^-50 of a turn while
+ * position * freqs[i] is below 2^50 turns; 16-bit rows then take 2^-26), the turn in fp32, one rounding
  * to the stored type; an e4m3 cache stores x / scale, clamped to [-448, 448], NaN kept.
  * q_out may be qkv itself (the turn in place; else they must not overlap).  A slot outside
  * the cache stores nothing; which of two tokens with one slot is kept is not defined.

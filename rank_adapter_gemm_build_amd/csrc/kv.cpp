@@ -22,7 +22,7 @@ using rax::timer_for;
 struct lora_rotary {
   int device = 0, rot = 0, interleaved = 0;
   float amplitude = 1.f;
-  double* turns = nullptr;   // device, [rot / 2]
+  double* turns = nullptr;   // device, [rot / 2][2]
 };
 
 struct lora_attention {
@@ -48,6 +48,7 @@ AttnRows attention_rows(long long rows, long long heads) {
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr double kPerTurn = 0x1.45f306dc9c883p-3, kPerTurnLow = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
 
 bool page_size_ok(int p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
 int log2_of(int p) {
@@ -222,10 +223,11 @@ lora_status lora_rotary_create(lora_rotary** out, int device, int rot_dim, int i
   lora_status st = check_rot(rot_dim);
   if (st != LORA_OK) return st;
   if (!std::isfinite((float)amplitude)) return fail(LORA_ERR_INVALID_ARG, "amplitude must be finite");
-  double turns[LORA_MAX_HEAD_DIM / 2];
+  double turns[LORA_MAX_HEAD_DIM];
   for (int i = 0; i < rot_dim / 2; ++i) {
     if (!std::isfinite(freqs[i])) return fail(LORA_ERR_INVALID_ARG, "freqs[%d] is not finite", i);
-    turns[i] = freqs[i] / kTwoPi;
+    turns[2 * i] = freqs[i] * kPerTurn;
+    turns[2 * i + 1] = std::fma(freqs[i], kPerTurn, -turns[2 * i]) + freqs[i] * kPerTurnLow;
   }
   if ((st = check_device(device)) != LORA_OK) return st;
   DeviceGuard g(device);
@@ -236,7 +238,7 @@ lora_status lora_rotary_create(lora_rotary** out, int device, int rot_dim, int i
   r->rot = rot_dim;
   r->interleaved = interleaved != 0;
   r->amplitude = (float)amplitude;
-  const size_t bytes = sizeof(double) * (rot_dim / 2);
+  const size_t bytes = sizeof(double) * rot_dim;
   hipError_t e = hipMalloc(reinterpret_cast<void**>(&r->turns), bytes);
   if (e == hipSuccess) e = hipMemcpy(r->turns, turns, bytes, hipMemcpyHostToDevice);
   if (e != hipSuccess) {

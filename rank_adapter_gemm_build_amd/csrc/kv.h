@@ -28,7 +28,7 @@ struct RotaryArgs {
   const void* qkv;
   void* q_out;
   const int32_t *positions, *slots;
-  const double* turns;   // [rot / 2]: turns a position
+  const double* turns;   // [rot / 2][2]: turns a position, as a sum of two
   CacheView c;
   int ldqkv, ldq, dtype, q_heads, num_tokens, rot, interleaved;
   float amplitude;
