@@ -54,6 +54,12 @@ def _elsewhere(device: int, *named) -> None:
             raise ValueError(f"{what} must be a tensor on cuda:{device}")
 
 
+def _c_int(value: int, what: str) -> None:
+    """A number that the C interface takes as an int (it would wrap)."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{what} = {value} does not fit 32 bits")
+
+
 def _vec(t, least: int, what: str) -> int:
     """Address of a contiguous int32 vector of at least `least` entries."""
     try:
@@ -82,9 +88,9 @@ def _table(t, rows: int) -> tuple:
         if cols > 1 and unit != 1:
             raise ValueError("block_table must have unit column stride")
         if shape[0] == 1:
-            ld = max(ld, cols)
-        elif ld < cols:
-            raise ValueError(f"block_table: row stride {ld} is below its width {cols}")
+            ld = cols   # the stride of a single row is never used
+        elif not cols <= ld < 2 ** 31:
+            raise ValueError(f"block_table: row stride {ld} is not in [{cols} (its width), 2^31)")
         return t.data_ptr(), ld, cols
     except AttributeError:
         raise TypeError("block_table must be a torch tensor") from None
@@ -101,9 +107,9 @@ def _rows(t, dtype, rows: int, width: int, what: str) -> tuple:
         if unit != 1 and width > 1:
             raise ValueError(f"{what} must have unit column stride (got stride {t.stride()})")
         if rows <= 1:
-            ld = -(-max(ld, width) // 8) * 8   # the stride of a single row is never used
-        elif ld < width:
-            raise ValueError(f"{what}: row stride {ld} is below its width {width}")
+            ld = -(-width // 8) * 8   # the stride of a single row is never used
+        elif not width <= ld < 2 ** 31:
+            raise ValueError(f"{what}: row stride {ld} is not in [{width} (its width), 2^31)")
         return t.data_ptr(), ld
     except AttributeError:
         raise TypeError(f"{what} must be a torch tensor") from None
@@ -197,6 +203,7 @@ def page_plan(plan: PagePlan, past_lens, new_lens, num_tokens: int, free_pages, 
     ring, cur = _vec(free_pages, 1, "free_pages"), _vec(cursor, 4, "cursor")
     cur_out = cur if cursor_out is None else _vec(cursor_out, 2, "cursor_out")
     table, ld, cols = _table(block_table, n)
+    _c_int(page_size, "page_size")
     if (past_lens.get_device() != dev or new_lens.get_device() != dev or free_pages.get_device() != dev or
             cursor.get_device() != dev or block_table.get_device() != dev or
             (cursor_out is not None and cursor_out.get_device() != dev)):
@@ -270,6 +277,9 @@ class Attention:
 
     def __init__(self, device: int, max_seqs: int, max_tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int):
         self.handle = 0
+        for value, what in ((max_seqs, "max_seqs"), (max_tokens, "max_tokens"), (num_q_heads, "num_q_heads"),
+                            (num_kv_heads, "num_kv_heads"), (head_dim, "head_dim")):
+            _c_int(value, what)
         self.device, self.max_seqs, self.max_tokens = device, max_seqs, max_tokens
         self.num_q_heads, self.num_kv_heads, self.head_dim = num_q_heads, num_kv_heads, head_dim
         h = C.c_void_p()
@@ -303,6 +313,7 @@ def paged_attention(attention: Attention, q, cache: KVCache, block_table, seq_le
     table, ld, cols = _table(block_table, n)
     T = q.shape[0] if hasattr(q, "shape") and len(q.shape) else 0
     width = attention.num_q_heads * attention.head_dim
+    _c_int(window, "window")
     qp, ldq = _rows(q, cache.act, T, width, "q")
     op, ldo = _rows(out, cache.act, T, width, "out")
     lp = None
