@@ -204,12 +204,14 @@ def page_plan(plan: PagePlan, past_lens, new_lens, num_tokens: int, free_pages, 
     cur_out = cur if cursor_out is None else _vec(cursor_out, 2, "cursor_out")
     table, ld, cols = _table(block_table, n)
     _c_int(page_size, "page_size")
+    lens, starts, positions, slots, meta = plan._out
+    if lens - 4 * n < past < lens + 4 * n or lens - 4 * n < new < lens + 4 * n:
+        raise ValueError("past_lens and new_lens must not overlap plan.seq_lens, which the call writes")
     if (past_lens.get_device() != dev or new_lens.get_device() != dev or free_pages.get_device() != dev or
             cursor.get_device() != dev or block_table.get_device() != dev or
             (cursor_out is not None and cursor_out.get_device() != dev)):
         _elsewhere(dev, ("past_lens", past_lens), ("new_lens", new_lens), ("free_pages", free_pages), ("cursor", cursor),
                    ("block_table", block_table), ("cursor_out", cursor_out))
-    lens, starts, positions, slots, meta = plan._out
     _check(lib.lora_page_plan(dev, past, new, n, num_tokens, page_size, free_pages.numel(), ring, cur, cur_out, table, ld,
                               cols, lens, starts, positions, slots, meta, _stream_on(dev, stream)), "lora_page_plan")
 

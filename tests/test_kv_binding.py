@@ -71,3 +71,16 @@ def test_sizes_past_31_bits_are_refused(monkeypatch):
     with pytest.raises(ValueError, match="page_size"):
         rx.page_plan(plan, torch.zeros(3, dtype=I32), torch.zeros(3, dtype=I32), 8, torch.zeros(8, dtype=I32), torch.zeros(4, dtype=I32),
                      torch.zeros(3, 4, dtype=I32), 2 ** 32 + 16)
+
+
+@pytest.mark.parametrize("which,at", [("past", 0), ("past", 2), ("new", 0), ("new", 1)])
+def test_lengths_that_the_plan_itself_writes_are_refused(monkeypatch, which, at):
+    """A step's workgroups read past_lens and new_lens while another writes seq_lens."""
+    monkeypatch.setattr(rx.kv, "lib", _NoCalls())
+    out = {k: torch.zeros(n, dtype=I32) for k, n in dict(seq_lens=5, query_start=6, positions=8, slots=8, meta=8).items()}
+    plan = _object(rx.PagePlan, device=0, max_seqs=5, max_tokens=8, _out=[t.data_ptr() for t in out.values()], **out)
+    lens = dict(past=torch.zeros(3, dtype=I32), new=torch.zeros(3, dtype=I32))
+    lens[which] = plan.seq_lens[at:at + 3]
+    with pytest.raises(ValueError, match="overlap"):
+        rx.page_plan(plan, lens["past"], lens["new"], 8, torch.zeros(8, dtype=I32), torch.zeros(4, dtype=I32),
+                     torch.zeros(3, 4, dtype=I32), 16)
