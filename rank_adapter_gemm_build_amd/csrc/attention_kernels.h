@@ -307,10 +307,8 @@ __global__ __launch_bounds__(64 * W, DB > 128 ? 1 : 2) void paged_attention_kern
   for (int i = r0; i < r1; ++i) sums[i] = by_unit ? whole_sums[i] + units_before : sums[i] + before;
   const int step_log2 = a.step_log2 + (by_unit ? kWholeLog2 : 0), tiles_log2 = step_log2 - kKeysLog2;   // tiles of a step
   const int workers_ = by_unit ? work_ : min((work_ + a.min_steps - 1) / a.min_steps, (int)gridDim.x);
-  // neighbouring shares on one XCD (the row blocks of a head read its keys from one L2), and
-  // as many on each
-  const int per_xcd = (workers_ + kXcds - 1) / kXcds, place = (int)(blockIdx.x / kXcds);
-  const int b_ = place < per_xcd ? (int)(blockIdx.x % kXcds) * per_xcd + place : workers_;
+  static_assert(kDies == kXcds, "shares are dealt over the XCDs");
+  const int b_ = share_of_block((int)blockIdx.x, workers_);
   if (b_ >= workers_) return;
   lds_barrier();
 

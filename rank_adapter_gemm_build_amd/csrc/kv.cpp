@@ -322,8 +322,7 @@ lora_status lora_attention_create(lora_attention** out, int device, int max_seqs
   lora_attention* a = new (std::nothrow) lora_attention;
   if (!a) return fail(LORA_ERR_OOM, "out of host memory");
   a->device = device;
-  // two workgroups a compute unit fit in registers and LDS
-  a->workers = std::min(512, std::max(8, 2 * cus / 8 * 8));
+  a->workers = rax::attention_workers(cus);
   a->max_seqs = max_seqs;
   a->max_tokens = max_tokens;
   a->q_heads = num_q_heads;

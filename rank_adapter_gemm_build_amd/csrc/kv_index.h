@@ -124,6 +124,21 @@ RAX_HD int line_step_log2(int least, int num_seqs, int num_tokens, int max_len, 
   return s <= 30 ? s : -1;
 }
 
+// Workgroups of the attention on a device of `cus` compute units: two each, as fit in registers and
+// LDS, half of them above 128 dims.  Both numbers are multiples of the dies, over which neighbouring
+// workgroups are dealt in turn: share_of_block needs that to reach every share.
+constexpr int kDies = 8;
+inline int attention_workers(int cus) {
+  const int w = 2 * cus / (2 * kDies) * (2 * kDies);
+  return w < 2 * kDies ? 2 * kDies : (w > 512 ? 512 : w);
+}
+// The share of workgroup `block`, or `workers` if it has none: neighbouring shares on one die (the
+// row blocks of a head read its keys from one L2), and as many on each.
+RAX_HD int share_of_block(int block, int workers) {
+  const int per = (workers + kDies - 1) / kDies, place = block / kDies;
+  const int b = place < per ? block % kDies * per + place : workers;
+  return b < workers ? b : workers;
+}
 // Contiguous equal shares of `work` steps: worker b of g takes [share_start(b), share_start(b + 1)).
 RAX_HD int share_start(int work, int g, int b) {
   const unsigned q = (unsigned)work / (unsigned)g, rem = (unsigned)work - q * (unsigned)g;
