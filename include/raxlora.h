@@ -601,7 +601,8 @@ lora_status lora_paged_attention(const lora_attention* attention, const void* q,
  * --debug: libraxlora_debug.so) checks, in its kernels, every index it takes from
  * memory (token ids, slots, sorted positions, workspace rows) against its range; a
  * failed check is counted and the access goes to index 0 instead, so a wrong index
- * shows as a count rather than a fault.  *enabled = 1 in such a build, 0 otherwise
+ * shows as a count rather than a fault.  (The page plan, rotary append and paged attention
+ * take wrong words as their contracts say, in every build, and count nothing here.)  *enabled = 1 in such a build, 0 otherwise
  * (where *faults is always 0); *faults = the checks failed on the current device since
  * the last reset (all kernels of the library, after the work enqueued so far has
  * finished: the call synchronises the device); reset != 0 clears the count.

@@ -104,7 +104,7 @@ template <int N, int AUX = 0> __device__ __forceinline__ Words<N> load_words(__a
 // A pair of loads covers 128 bytes of each of 16 keys.  Each load takes whole lines, of 8 keys
 // (streamed lines that two loads touch cost more: 64 sequences to 8192, e4m3 rows of 128
 // bytes, 118 -> 108 us, bf16 to 4096 106.5 -> 102.3; rows that follow each other in memory
-// within 2 % either way; 256-byte pieces of 4 keys no better): lane c16 of `a` holds key c16 % 8, of `b` 8 + c16 % 8, bytes 64 (c16 / 8)
+// within 2 % either way; heads of 80, whose rows are not whole lines, 93 -> 94; 256-byte pieces of 4 keys no better): lane c16 of `a` holds key c16 % 8, of `b` 8 + c16 % 8, bytes 64 (c16 / 8)
 // on.  The matrix cores' operands have key c16 in lane c16, the first 64 bytes in one and the
 // others in the next, so the lanes of a row of 16 exchange with those 8 away.
 __device__ __forceinline__ void whole_keys(uint4& a, uint4& b) {

@@ -35,7 +35,7 @@ struct lora_attention {
 namespace rax {
 // Larger blocks read the keys fewer times, but where there are few units each is cut into
 // many parts, whose join one workgroup does: the more blocks, the more of those.  Measured
-// with blocks of 64, 32, 16 rows: 64 rows of 32 x 8 heads 116, 114, 185 us, of 64 x 8 heads
+// (sequences of equal numbers of rows) with blocks of 64, 32, 16 rows: 64 rows of 32 x 8 heads 116, 114, 185 us, of 64 x 8 heads
 // 174, 213, 330; of 1 x 8 heads 77, 46, 31; 32 rows of 16 x 8 heads (-, 55, 62).  Four row
 // waves (128 rows) were slower than two everywhere (128 rows of 128 x 4 heads 205 us, 149).
 AttnRows attention_rows(long long rows, long long heads) {
