@@ -69,6 +69,14 @@ def test_plan_with_wrong_words_writes_its_outputs_only(seqs, cursor):
         np.testing.assert_array_equal(got["ring"], wring)
 
 
+def test_plan_counts_only_pages_that_were_drawn():
+    """Request 0 starts a page and there is none; request 1 fits its last page and is granted: the ring stays."""
+    got, tab = plan_between_margins([16, 5], [1, 1], [[2, -1], [0, -1]], 2, [1, 3, 1, 3], [3, 0], 16, 2)
+    assert got["seq_lens"].tolist() == [0, 6] and got["slots"].tolist() == [-1, 5] and got["positions"].tolist() == [16, 5]
+    assert got["cursor_out"].tolist() == [3, 0] and got["meta"].tolist() == [2, 0, 0, 1, 0, 0, 0, 0]
+    assert tab.tolist() == [[2, -1], [0, -1]] and got["ring"].tolist() == [1, 3, 1, 3]
+
+
 # =============================================================================== rotary append
 @pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("rot", [64, 22])
