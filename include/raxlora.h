@@ -597,6 +597,92 @@ lora_status lora_paged_attention(const lora_attention* attention, const void* q,
                                  float scale, int window, void* out, int ldo, float* lse, hipStream_t stream);
 
 /*
+ * ---- Beam search, and batches with common tokens, over the paged cache ----
+ *
+ * Beam selection picks every request's best continuations, the page fork lets block table rows follow
+ * their beams, the page copy moves the cells that a fork must not share, and the shared attention
+ * reads pages that several sequences hold once for all of them.  Conventions as above.
+ */
+#define LORA_MAX_BEAMS   64         /* beams, and candidates, of a request */
+#define LORA_MAX_VOCAB   (1 << 24)
+#define LORA_FORK_META   8          /* words of lora_page_fork's meta */
+#define LORA_MAX_LAYERS  128        /* layers of one lora_page_copy */
+
+/*
+ * Beam selection for up to max_requests requests of `beams` beams each (owns the workspace).
+ * Errors of create: out NULL -> INVALID_ARG; max_requests outside [1, LORA_MAX_SEQS], beams or
+ * candidates outside [1, LORA_MAX_BEAMS], vocab outside [1, LORA_MAX_VOCAB] -> SHAPE; NO_DEVICE / OOM.
+ */
+typedef struct lora_beams lora_beams;
+lora_status lora_beams_create(lora_beams** out, int device, int max_requests, int beams, int vocab, int candidates);
+lora_status lora_beams_destroy(lora_beams* beams);
+
+/*
+ * The best continuations of each request.  Row b = request * beams + beam has logits[b][0..vocab) (row
+ * stride ldlogits, LORA_BF16 or LORA_F32) and the score scores[b] so far; its candidate of token v has the score
+ *   s(b, v) = scores[b] + logits[b][v] - ln sum_u exp logits[b][u].
+ * A row with ended[b] != 0 (ended may be NULL) has one candidate, end_token with the score scores[b], and its
+ * logits are not read; nor are those of a row whose score is -inf or NaN, which has none.  Candidates rank by s, or by
+ * weights[b] s (weights may be NULL; a row whose weight is not above 0 has no candidates): the
+ * larger first, of equal ones the lower row, within a row the larger logit, of equal ones the lower token.
+ * Candidates whose score is -inf or NaN are not chosen (a logit of -inf; any of a row whose logits
+ * hold NaN or +inf or are all -inf).
+ * Written, for c < candidates in order of rank: parents[request * candidates + c] = the row (lora_page_fork
+ * takes it), tokens, scores_out = s, and ended_out (may be NULL) = 1 if the row had ended or the token is
+ * end_token, else 0; for places without a candidate -1, -1, -inf, 0.
+ * Exponentials are summed in fp32 relative to maxima kept by each lane (2^-18 of the sum at most, 2^-27 as a
+ * rule), the rest and the scores that rank are in 64 bits, scores_out is rounded once.  The result is the same on every call.
+ * With candidates = beams, scores_out may be scores and ended_out may be ended; else outputs overlap nothing.
+ * end_token: in [0, vocab), or -1 for none where ended is NULL.  One launch on `stream`; two
+ * calls on one object must not overlap in time.  Errors: INVALID_ARG (NULL, end_token, outputs that overlap), SHAPE
+ * (num_requests < 0, ldlogits < vocab), CAPACITY (num_requests above the object's), DTYPE, ALIGN (logits).
+ */
+lora_status lora_beam_select(const lora_beams* beams, const void* logits, int ldlogits, lora_dtype dtype, const float* scores,
+                             const int32_t* ended, int end_token, const float* weights, int num_requests, int32_t* parents,
+                             int32_t* tokens, float* scores_out, int32_t* ended_out, hipStream_t stream);
+
+/*
+ * Row i of the block table becomes a continuation of what row parents[i] was before the call (-1:
+ * row i becomes empty), in place, with pages shared: shares[num_pages] holds, for every page, the number of its holders
+ * beyond the first (0 for pages with one holder, and for free ones: pages that lora_page_plan draws need no care).
+ * lens[num_rows]: tokens in the cache; in, of the old rows, out, of the new ones.  free_pages and cursor: the ring
+ * of lora_page_plan.
+ *   - Full pages of a row pass to all its children.  A partly filled last page, which its row holds alone, passes to
+ *     the first child; every other child draws a page from the ring, in order of the children, and the cells that it
+ *     needs are listed: copy_src[i], copy_dst[i], copy_tokens[i] (-1, -1, 0 for other rows; lora_page_copy takes them).
+ *     Children past the number of free pages are refused: their rows become empty.
+ *   - Pages that lose their last holder go to the ring's end, in ascending order; the call itself does not
+ *     draw them.
+ * With parents = -1 for the rows of requests that have ended the call frees what only they held (lora_page_plan's
+ * new_lens = -1 would give shared pages back as well, and is for rows without shares).  A new row's
+ * entries past its length are left as they were.
+ * meta[LORA_FORK_META] = pages drawn, pages given back, rows refused, invalid entries, free pages after, 0, 0, 0.
+ * Invalid entries: a parent outside [-1, num_rows) (taken as -1), a length outside [0, max_pages * page_size] (the
+ * row holds nothing), a page id outside [0, num_pages) in the used part of a row or among the drawn (-1 in the new
+ * row, nothing copied), pages given back beyond the ring's places.  scratch[(num_pages + 31) / 32] and cursor[2..3] are scratch words,
+ * zero between calls.  No vector may overlap another.  Rows may name any row as parent, several the same.
+ * One launch on `stream` of `device`; two calls that share a cursor, or a call and a page plan, must not overlap in time.
+ * Errors: INVALID_ARG (a NULL pointer), SHAPE (num_rows outside [0, LORA_MAX_SEQS], page_size, num_pages, max_pages,
+ * ld_table as lora_page_plan).  num_rows = 0 does nothing.
+ */
+lora_status lora_page_fork(int device, const int32_t* parents, int num_rows, int32_t* lens, int page_size, int num_pages,
+                           int32_t* free_pages, int32_t* cursor, int32_t* shares, int32_t* block_table, int ld_table,
+                           int max_pages, int32_t* copy_src, int32_t* copy_dst, int32_t* copy_tokens, int32_t* scratch,
+                           int32_t* meta, hipStream_t stream);
+
+/*
+ * The keys and values of the first tokens[i] tokens (all of them if tokens is NULL; a number outside [0,
+ * page_size] is taken as the nearer bound) of page src[i] go to page dst[i], for num_pairs pairs, in every one of num_layers
+ * caches, which differ in k and v only.  Pairs with a page outside the cache, or twice the same, copy nothing.
+ * A page may be the source of several pairs; one that is written must not be in another pair.  src, dst, tokens: device
+ * int32 [num_pairs].  One launch on `stream` of `device`.
+ * Errors: INVALID_ARG (NULL), SHAPE (num_layers outside [1, LORA_MAX_LAYERS], num_pairs outside [0, 2^20], layers that
+ * differ, the cache's rules), DTYPE, ALIGN.
+ */
+lora_status lora_page_copy(int device, const lora_kv_cache* layers, int num_layers, const int32_t* src, const int32_t* dst,
+                           const int32_t* tokens, int num_pairs, hipStream_t stream);
+
+/*
  * Index checks (diagnostics): a library built with -DRAXLORA_DEBUG (build.py
  * --debug: libraxlora_debug.so) checks, in its kernels, every index it takes from
  * memory (token ids, slots, sorted positions, workspace rows) against its range; a
@@ -624,14 +710,13 @@ lora_status lora_bandwidth_probe(const void* src, uint64_t read_bytes, void* dst
 
 /*
  * Kernel timing (diagnostics).  While enabled (process-wide), every kernel that
- * the routing, shrink, expand, linear, embedding, page plan, rotary append and paged
- * attention calls launch is started
+ * the routing, shrink, expand, linear, embedding, paged-cache and beam search calls launch is started
  * with hipExtLaunchKernel and a pair of events stamped at that kernel's own start
  * and end, on the stream it runs on.  lora_timing_report waits for the recorded
  * events, writes per kernel id (0 routing, 1 shrink, 2 expand, 3 finish_u: the
  * pass of lora_shrink that adds the k-split partial sums into the caller's u,
  * 4 gather: the embedding rows of lora_embedding, 5 page_plan, 6 rotary_append, 7
- * attention; the shrink and expand launches cover both short and long segments) the summed milliseconds and the
+ * attention, 8 beam_select, 9 page_fork, 10 page_copy, 11 shared_attention, 12 shared_merge; the shrink and expand launches cover both short and long segments) the summed milliseconds and the
  * number of launches into total_ms[0..max_kernels) and launches[0..max_kernels), and
  * clears the record.  lora_timing_kernel_name gives the name of an id ("" if none).
  * Errors: INVALID_ARG for NULL arrays with max_kernels > 0; HIP if an event fails.

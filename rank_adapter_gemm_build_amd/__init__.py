@@ -81,12 +81,18 @@ SIGNATURES = {
     "lora_attention_destroy": (_I, [_P]),
     "lora_paged_attention": (_I, [_P, _VP, _I, _I, C.POINTER(_CKVCache), _VP, _I, _I, _VP, _VP, _I, _I, _F, _I, _VP, _I,
                                   _VP, _VP]),
+    "lora_beams_create": (_I, [C.POINTER(_P), _I, _I, _I, _I, _I]),
+    "lora_beams_destroy": (_I, [_P]),
+    "lora_beam_select": (_I, [_P, _VP, _I, _I, _VP, _VP, _I, _VP, _I, _VP, _VP, _VP, _VP, _VP]),
+    "lora_page_fork": (_I, [_I, _VP, _I, _VP, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "lora_page_copy": (_I, [_I, C.POINTER(_CKVCache), _I, _VP, _VP, _VP, _I, _VP]),
     "lora_timing_enable": (_I, [_I]),
     "lora_timing_report": (_I, [C.POINTER(C.c_double), C.POINTER(C.c_int), _I]),
     "lora_timing_kernel_name": (C.c_char_p, [_I]),
 }
 
-KERNEL_NAMES = ["routing", "shrink", "expand", "finish_u", "gather", "page_plan", "rotary_append", "attention"]
+KERNEL_NAMES = ["routing", "shrink", "expand", "finish_u", "gather", "page_plan", "rotary_append", "attention",
+                "beam_select", "page_fork", "page_copy", "shared_attention", "shared_merge"]
 
 
 def _load():
@@ -648,3 +654,6 @@ def route_linear_group(pools, routing: Routing, ids, xs, ys, stream=None) -> Non
 # the paged-cache operators (page plan, rotary append, paged attention)
 from .kv import *  # noqa: E402,F401,F403
 from . import kv  # noqa: E402,F401
+# the operators of beam search over the paged cache (beam selection, page fork and copy, shared attention)
+from .beam import *  # noqa: E402,F401,F403
+from . import beam  # noqa: E402,F401

@@ -164,7 +164,8 @@ KTimer timer_for(int kernel) {
 namespace {
 
 const char* const kKernelNames[rax::kKernelCount] = {"routing",  "shrink",    "expand",        "finish_u",
-                                                      "gather",   "page_plan", "rotary_append", "attention"};
+                                                      "gather",   "page_plan", "rotary_append", "attention",
+                                                      "beam_select", "page_fork", "page_copy", "shared_attention", "shared_merge"};
 
 int env_int(const char* name, int dflt) {
   const char* v = getenv(name);

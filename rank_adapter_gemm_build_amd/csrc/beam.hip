@@ -1,0 +1,357 @@
+// Beam selection: of a request's beams b and tokens v the `best` candidates with the largest
+// w_b s(b, v), s(b, v) = score_b + x[b][v] - ln sum_u exp x[b][u], in one pass over the logits.
+//
+// Within a row the order of the candidates is that of the logits, so a row's best are found and
+// its log sum is formed side by side while the row streams by, and only the joining of rows needs
+// the sums.  A workgroup has a share of one row.  Of each request the last workgroup to finish
+// joins: it forms the rows' log sums and picks among the shares' lists.
+//
+// Sum.  Each lane keeps a maximum and the sum of exponentials relative to it; a lane's largest
+// term is then exactly 1, and lanes, waves and shares are joined in 64 bits, so the few terms
+// that make up a peaked distribution's sum carry no rounding of an exponential.  Scores are
+// formed in 64 bits: candidates of two beams may lie next to each other.
+//
+// Lists.  A candidate is one 64-bit word that sorts as (row, value, token) do: complement of the
+// row, value as an ordered integer, complement of the token.  A wave appends to its list in LDS
+// what is not below its `floor`: at first the best-th largest of its lanes' maxima, then the
+// best-th entry of the list itself whenever that is cut back to `best` (each entry's place is the
+// number of larger ones).  After the first tile hits are rare, and a tile costs little more
+// than its exponentials.
+//
+// What bounds it: reading the logits; next to that the exponential, 4 of some 12 vector
+// cycles a value.
+#include <hip/hip_runtime.h>
+
+#include <cfloat>
+#include <cmath>
+
+#include "beam.h"
+#include "device_util.h"
+
+namespace rax {
+
+namespace {
+
+typedef unsigned long long u64;
+constexpr int kBeamThreads = 64 * kBeamWaves;
+constexpr int kListCap = LORA_MAX_BEAMS + 64 * 8;   // a list's `best` and one load of every lane
+constexpr float kLog2e = 1.44269504088896341f;
+
+struct Entry {   // a candidate of the join
+  double rank;
+  u64 key;
+};
+
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u ^ (~(uint32_t)((int)u >> 31) | 0x80000000u)); }
+// never 0: a value in a list is at least -FLT_MAX
+__device__ __forceinline__ u64 key_of(int row, float v, int token) {
+  return (u64)(63 - row) << 56 | (u64)ordered(v + 0.f) << 24 | (0xffffffu - (uint32_t)token);   // -0 as 0
+}
+__device__ __forceinline__ float key_value(u64 key) { return unordered((uint32_t)(key >> 24)); }
+__device__ __forceinline__ int key_token(u64 key) { return (int)(0xffffffu - (uint32_t)(key & 0xffffffu)); }
+__device__ __forceinline__ int key_row(u64 key) { return 63 - (int)(key >> 56); }
+
+__device__ __forceinline__ u64 get_word(const u64* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ void put_word(u64* p, u64 v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ double get_double(const double* p) { return __longlong_as_double((long long)get_word(reinterpret_cast<const u64*>(p))); }
+__device__ __forceinline__ void put_double(double* p, double v) { put_word(reinterpret_cast<u64*>(p), (u64)__double_as_longlong(v)); }
+
+// the n-th largest of the lanes' keys, 0 if n is above 64
+__device__ __forceinline__ uint32_t nth_of_lanes(uint32_t key, int n) {
+  uint32_t at = 0;
+#pragma unroll
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t test = at | 1u << bit;
+    if (__popcll(__ballot(key >= test)) >= n) at = test;
+  }
+  return at;
+}
+
+template <typename T> struct Chunk;   // 16 bytes of logits
+template <> struct Chunk<uint16_t> {
+  static constexpr int kN = 8;
+  static constexpr uint32_t kNone = 0xff80ff80u;
+  __device__ __forceinline__ static float at(const uint4& c, int e) {
+    const uint32_t w = (&c.x)[e / 2];
+    return e & 1 ? bf16_hi(w) : bf16_lo(w);
+  }
+};
+template <> struct Chunk<float> {
+  static constexpr int kN = 4;
+  static constexpr uint32_t kNone = 0xff800000u;
+  __device__ __forceinline__ static float at(const uint4& c, int e) { return __uint_as_float((&c.x)[e]); }
+};
+
+// Cut a wave's list of n entries back to its `best` largest, in order; returns their number.
+__device__ __forceinline__ int cut_list(u64* list, u64* sorted, int n, int best, int lane) {
+  if (lane == 0) list[n] = 0;   // entries are read two at a time
+  wave_lds_sync();
+  for (int i = lane; i < n; i += 64) {
+    const u64 mine = list[i];
+    int place = 0;
+    for (int j = 0; j < n; j += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(list + j);
+      place += (two.x > mine) + (two.y > mine);
+    }
+    if (place < best) sorted[place] = mine;
+  }
+  wave_lds_sync();
+  n = min(n, best);
+  if (lane < n) list[lane] = sorted[lane];
+  wave_lds_sync();
+  return n;
+}
+
+}  // namespace
+
+template <typename T>
+__global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
+  using C = Chunk<T>;
+  constexpr int N = C::kN, U = kBeamLoads;
+  __shared__ __attribute__((aligned(16))) u64 lists[kBeamWaves][kListCap + 2 + LORA_MAX_BEAMS];
+  __shared__ double wave_sums[kBeamWaves][2], lse_s[LORA_MAX_BEAMS];
+  __shared__ int counts[kBeamWaves], last_s, count_s;
+  const int tid = threadIdx.x, lane = lane_id(), w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs, request = row / a.beams, beam = row - request * a.beams;
+  const int best = a.best;
+
+  // ---- this workgroup's share of the row.  Loads are of aligned 16 bytes; a row that begins
+  // inside one has its first and last values fetched singly.
+  const T* const x = reinterpret_cast<const T*>(a.logits) + (size_t)row * a.ld;
+  const int shift = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+  const uint4* const chunks = reinterpret_cast<const uint4*>(x - shift);
+  const auto load = [&](int tile, uint4 (&c)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int first = ((tile * U + u) * 64 + lane) * N - shift;   // token of the chunk's first value
+      c[u] = make_uint4(C::kNone, C::kNone, C::kNone, C::kNone);
+      if (first >= 0 && first + N <= a.vocab) {
+        c[u] = chunks[(tile * U + u) * 64 + lane];
+      } else if (first > -N && first < a.vocab) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (first + e >= 0 && first + e < a.vocab) {
+            if constexpr (sizeof(T) == 4) (&c[u].x)[e] = __float_as_uint(x[first + e]);
+            else {
+              uint32_t& word = (&c[u].x)[e / 2];
+              word = e & 1 ? (word & 0xffffu) | (uint32_t)x[first + e] << 16 : (word & 0xffff0000u) | x[first + e];
+            }
+          }
+      }
+    }
+  };
+  const int tile_n = 64 * U * N, tiles = (a.vocab + shift + tile_n - 1) / tile_n, stride = a.segs * kBeamWaves;
+  int tile = seg * kBeamWaves + w;
+  uint4 cur[U], nxt[U];
+  load(tile, cur);
+  const float score = a.scores[row];
+  const bool live = score > -INFINITY && !(a.ended && a.ended[row]);   // else the row is not read
+  if (live) {
+    u64 *list = lists[w], *sorted = list + kListCap + 2;
+    float m = -INFINITY, l = 0.f, floor_ = -FLT_MAX;
+    int n = 0;
+    for (bool first = true; tile < tiles; tile += stride, first = false) {
+      if (tile + stride < tiles) load(tile + stride, nxt);
+      float top[U], all = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        top[u] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < N; ++e) top[u] = fmaxf(top[u], C::at(cur[u], e));
+        all = fmaxf(all, top[u]);
+      }
+      const float mn = fmaxf(m, all), base = mn == -INFINITY ? 0.f : mn;
+      l *= __builtin_amdgcn_exp2f((m - base) * kLog2e);
+      m = mn;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float part = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) part += __builtin_amdgcn_exp2f((C::at(cur[u], e) - base) * kLog2e);
+        l += part;
+      }
+      if (first) floor_ = fmaxf(floor_, unordered(nth_of_lanes(ordered(all), best)));
+      if (__any(all >= floor_)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (!__any(top[u] >= floor_)) continue;
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const float v = C::at(cur[u], e);
+            const bool hit = v >= floor_;
+            const u64 mask = __ballot(hit);
+            if (mask == 0) continue;
+            if (hit) list[n + __popcll(mask & ((1ull << lane) - 1ull))] = key_of(beam, v, ((tile * U + u) * 64 + lane) * N + e - shift);
+            n += __popcll(mask);
+          }
+          if (n > LORA_MAX_BEAMS) {   // room for another load; tokens to come are higher, so equal values no longer enter
+            n = cut_list(list, sorted, n, best, lane);
+            if (n == best) floor_ = unordered(ordered(key_value(list[best - 1])) + 1u);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u] = nxt[u];
+    }
+    n = cut_list(list, sorted, n, best, lane);
+    // the wave's sum
+    float wm = m;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) wm = fmaxf(wm, __shfl_xor(wm, d));
+    double wl = (double)l * (m == wm ? 1.0 : exp((double)m - (double)wm));   // m = -inf: 0
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) wl += __shfl_xor(wl, d);
+    if (lane == 0) {
+      counts[w] = n;
+      wave_sums[w][0] = wm;
+      wave_sums[w][1] = wl;
+    }
+    __syncthreads();
+    // the workgroup's list and sum
+    u64* out = a.keys + ((size_t)row * a.segs + seg) * best;
+    int total = 0;
+#pragma unroll
+    for (int v = 0; v < kBeamWaves; ++v) total += counts[v];
+    if (lane < n) {
+      const u64 mine = list[lane];
+      int place = 0;
+#pragma unroll
+      for (int v = 0; v < kBeamWaves; ++v)
+        for (int j = 0; j < counts[v]; ++j) place += lists[v][j] > mine;
+      if (place < best) put_word(out + place, mine);
+    }
+    if (tid >= total && tid < best) put_word(out + tid, 0);
+    if (tid == 0) {
+      double gm = wave_sums[0][0], gl = 0.0;
+#pragma unroll
+      for (int v = 1; v < kBeamWaves; ++v) gm = fmax(gm, wave_sums[v][0]);
+#pragma unroll
+      for (int v = 0; v < kBeamWaves; ++v)
+        gl += wave_sums[v][1] * (wave_sums[v][0] == gm ? 1.0 : exp(wave_sums[v][0] - gm));
+      double* s = a.sums + ((size_t)row * a.segs + seg) * 2;
+      put_double(s, gm);
+      put_double(s + 1, gl);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // every store of this wave has arrived
+  }
+  __syncthreads();
+  if (tid == 0) {
+    last_s = __hip_atomic_fetch_add(&a.arrived[request], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.beams * a.segs - 1;
+    if (last_s) __hip_atomic_store(&a.arrived[request], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    count_s = 0;
+  }
+  __syncthreads();
+  if (!last_s) return;
+
+  // ---- the request's join
+  __shared__ float score_s[LORA_MAX_BEAMS], weight_s[LORA_MAX_BEAMS];
+  __shared__ int over_s[LORA_MAX_BEAMS];   // 0: read, 1: ended, 2: gives no candidate
+  Entry *entries = reinterpret_cast<Entry*>(&lists[0][0]), *sorted = entries + kListCap;
+  const int row0 = request * a.beams;
+  if (tid < a.beams) {
+    const float c = a.scores[row0 + tid], q = a.weights ? a.weights[row0 + tid] : 1.f;
+    score_s[tid] = c;
+    weight_s[tid] = q;
+    over_s[tid] = !(c > -INFINITY) || !(q > 0.f) ? 2 : a.ended && a.ended[row0 + tid] ? 1 : 0;
+  }
+  __syncthreads();
+  for (int j = w; j < a.beams; j += kBeamWaves) {
+    if (over_s[j]) continue;
+    const double* s = a.sums + (size_t)(row0 + j) * a.segs * 2;
+    double jm = -INFINITY, jl = 0.0;
+    for (int i = lane; i < a.segs; i += 64) {
+      const double pm = get_double(s + 2 * i), pl = get_double(s + 2 * i + 1), nm = fmax(jm, pm);
+      jl = jl * (jm == nm ? 1.0 : exp(jm - nm)) + pl * (pm == nm ? 1.0 : exp(pm - nm));
+      jm = nm;
+    }
+    double top = jm;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d));
+    jl *= jm == top ? 1.0 : exp(jm - top);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) jl += __shfl_xor(jl, d);
+    if (lane == 0) lse_s[j] = top + log(jl);   // no finite logit, or one that is NaN or +inf: not a number, no candidate
+  }
+  __syncthreads();
+  const auto candidate = [&](u64 key) {
+    const int j = key_row(key);
+    return over_s[j] == 1 ? (double)score_s[j] : (double)score_s[j] + ((double)key_value(key) - lse_s[j]);
+  };
+  const int per_row = a.segs * best, n = a.beams * per_row;
+  Entry floor_{-INFINITY, 0};
+  bool full = false;
+  // ended beams are candidates of the first round, in place of a list
+  for (int i0 = -kBeamThreads; i0 < n; i0 += kBeamThreads) {
+    u64 key = 0;
+    if (i0 < 0) {
+      if (tid < a.beams && over_s[tid] == 1) key = key_of(tid, 0.f, a.end_token);
+    } else if (i0 + tid < n) {
+      const int j = (int)((unsigned)(i0 + tid) / (unsigned)per_row);
+      if (over_s[j] == 0) key = get_word(a.keys + (size_t)row0 * per_row + i0 + tid);
+    }
+    Entry e{0.0, key};
+    bool hit = false;
+    if (key) {
+      const double s = candidate(key);
+      e.rank = s * (double)weight_s[key_row(key)];
+      hit = s > -INFINITY && e.rank == e.rank && (!full || e.rank > floor_.rank || (e.rank == floor_.rank && key > floor_.key));
+    }
+    const u64 mask = __ballot(hit);
+    int at = 0;
+    if (lane == 0 && mask) at = atomicAdd(&count_s, __popcll(mask));
+    at = __shfl(at, 0) + __popcll(mask & ((1ull << lane) - 1ull));
+    if (hit) entries[at] = e;
+    __syncthreads();
+    const int c = count_s;
+    const bool end = i0 + kBeamThreads >= n;
+    if (c > kListCap - kBeamThreads || (end && c > 0)) {
+      for (int i = tid; i < c; i += kBeamThreads) {
+        const Entry mine = entries[i];
+        int place = 0;
+        for (int j = 0; j < c; ++j) {
+          const Entry o = entries[j];
+          place += o.rank > mine.rank || (o.rank == mine.rank && o.key > mine.key);
+        }
+        if (place < best) sorted[place] = mine;
+      }
+      __syncthreads();
+      const int kept = min(c, best);
+      if (tid < kept) entries[tid] = sorted[tid];
+      if (tid == 0) count_s = kept;
+      full = kept == best;
+      if (full) floor_ = sorted[best - 1];
+    }
+    __syncthreads();   // the count is read before the next round adds to it
+  }
+  const int found = count_s;
+  if (tid < best) {
+    const int out = request * best + tid;
+    int parent = -1, token = -1, done = 0;
+    float s = -INFINITY;
+    if (tid < found) {
+      const u64 key = entries[tid].key;
+      const int j = key_row(key);
+      parent = row0 + j;
+      token = key_token(key);
+      done = over_s[j] == 1 || token == a.end_token;
+      s = (float)candidate(key);
+    }
+    a.parents[out] = parent;
+    a.tokens[out] = token;
+    a.scores_out[out] = s;
+    if (a.ended_out) a.ended_out[out] = done;
+  }
+}
+
+hipError_t launch_beam_select(const BeamArgs& a, hipStream_t stream, const KTimer& tm) {
+  const dim3 grid((unsigned)(a.requests * a.beams * a.segs)), block(kBeamThreads);
+  if (a.dtype == LORA_F32) RAX_LAUNCH(tm, beam_select_kernel<float>, grid, block, 0u, stream, a);
+  else RAX_LAUNCH(tm, beam_select_kernel<uint16_t>, grid, block, 0u, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace rax

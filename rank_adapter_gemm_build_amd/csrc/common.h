@@ -159,7 +159,7 @@ struct KTimer {
 
 // kernels the timing facility reports, in this order
 enum KernelId { kKRouting = 0, kKShrink, kKExpand, kKFinish, kKGather, kKPagePlan, kKRotary,
-                kKAttention, kKernelCount };
+                kKAttention, kKBeam, kKFork, kKCopy, kKShared, kKMerge, kKernelCount };
 
 // launchers (device code in the .hip files); all return the launch status
 // ids: one per token (tps = 1) or one per sequence of tps consecutive tokens
