@@ -683,6 +683,37 @@ lora_status lora_page_copy(int device, const lora_kv_cache* layers, int num_laye
                            const int32_t* tokens, int num_pairs, hipStream_t stream);
 
 /*
+ * Shared attention for up to max_seqs sequences and max_tokens new tokens (owns the workspace: the two results
+ * of every row, 8 bytes * max_tokens * num_q_heads * (head_dim + 2), partial results of 1 MiB a head_dim value
+ * on 256 compute units, and counters).  Arguments and errors of create as lora_attention_create.
+ */
+typedef struct lora_shared lora_shared;
+lora_status lora_shared_create(lora_shared** out, int device, int max_seqs, int max_tokens,
+                                         int num_q_heads, int num_kv_heads, int head_dim);
+lora_status lora_shared_destroy(lora_shared* attention);
+
+/*
+ * lora_paged_attention (without a window) of sequences whose first tokens lie in common pages, which are read once for
+ * all of a group.  Group g has the sequences group_start[g] .. group_start[g + 1] - 1 and common_lens[g] common
+ * tokens: of each of its sequences these have the same keys and values.  A sequence takes part if its new tokens
+ * come after all of them (seq_lens - n >= common_lens[g]); the common keys are read by the block table row of the
+ * group's first sequence that does, and the other keys by the sequence's own.  A sequence that does not take part, one
+ * outside of all groups and one with common_lens 0 are as in lora_paged_attention.  common_lens need
+ * not be a multiple of the page size, nor all that the sequences share.  The result is bitwise the same on every call,
+ * and that of lora_paged_attention but for rounding: all sums are fp32, with one rounding to out.
+ * group_start: device int32 [num_groups + 1], rising; values outside [0, num_seqs] are taken as the nearer
+ * bound.  common_lens: device int32 [num_groups], taken as the nearer bound of [0, max_pages * page_size].  num_groups in
+ * [0, max_seqs of the object].  Two launches on `stream`.  Two calls on one object must not overlap in time.
+ * All else, errors among it, as lora_paged_attention; group_start and common_lens NULL with num_groups > 0 ->
+ * INVALID_ARG, num_groups negative -> SHAPE, above the object's max_seqs -> CAPACITY.
+ */
+lora_status lora_shared_attention(const lora_shared* attention, const void* q, int ldq, lora_dtype dtype,
+                                      const lora_kv_cache* cache, const int32_t* block_table, int ld_table, int max_pages,
+                                      const int32_t* seq_lens, const int32_t* query_start, int num_seqs, int num_tokens,
+                                      const int32_t* group_start, const int32_t* common_lens, int num_groups, float scale,
+                                      void* out, int ldo, float* lse, hipStream_t stream);
+
+/*
  * Index checks (diagnostics): a library built with -DRAXLORA_DEBUG (build.py
  * --debug: libraxlora_debug.so) checks, in its kernels, every index it takes from
  * memory (token ids, slots, sorted positions, workspace rows) against its range; a

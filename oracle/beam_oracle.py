@@ -1,13 +1,13 @@
 """Plain definitions of the operators of beam search over the paged cache in 64 bits, on the CPU (test infrastructure
 only; shares no code with the GPU path).  Written from the contract in include/raxlora.h: loops over rows,
-candidates, pages and heads."""
+candidates and pages."""
 from __future__ import annotations
 
 import math
 
 import numpy as np
 
-__all__ = ["log_sums", "select", "page_fork", "page_copy", "shared_attend"]
+__all__ = ["log_sums", "select", "page_fork", "page_copy"]
 
 
 def log_sums(logits):
@@ -121,3 +121,4 @@ def page_copy(cells, src, dst, tokens, page):
             n = page if tokens is None else min(max(int(tokens[i]), 0), page)
             out[b, :n] = cells[a, :n]
     return out
+

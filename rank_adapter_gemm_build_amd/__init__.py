@@ -86,6 +86,10 @@ SIGNATURES = {
     "lora_beam_select": (_I, [_P, _VP, _I, _I, _VP, _VP, _I, _VP, _I, _VP, _VP, _VP, _VP, _VP]),
     "lora_page_fork": (_I, [_I, _VP, _I, _VP, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP]),
     "lora_page_copy": (_I, [_I, C.POINTER(_CKVCache), _I, _VP, _VP, _VP, _I, _VP]),
+    "lora_shared_create": (_I, [C.POINTER(_P), _I, _I, _I, _I, _I, _I]),
+    "lora_shared_destroy": (_I, [_P]),
+    "lora_shared_attention": (_I, [_P, _VP, _I, _I, C.POINTER(_CKVCache), _VP, _I, _I, _VP, _VP, _I, _I, _VP, _VP, _I, _F,
+                                       _VP, _I, _VP, _VP]),
     "lora_timing_enable": (_I, [_I]),
     "lora_timing_report": (_I, [C.POINTER(C.c_double), C.POINTER(C.c_int), _I]),
     "lora_timing_kernel_name": (C.c_char_p, [_I]),

@@ -5,20 +5,23 @@ does between the logits and the next step's page plan, and the attention that re
     beam_select(beams, logits, scores, parents, tokens, scores)                           # once a step
     page_fork(plan, parents, lens, free_pages, cursor, shares, block_table, page_size)
     page_copy(layers, plan.copy_src, plan.copy_dst, plan.copy_tokens)
+    shared_attention(attention, q, cache, block_table, seq_lens, query_start, group_start, common_lens, out)   # per layer
 
 Imported by the package itself; argument checks and marshalling only."""
 from __future__ import annotations
 
 import ctypes as C
+import math
+from typing import Optional
 
 from . import LORA_BF16, LORA_F32, _check, _CKVCache, lib
 from . import kv
-from .kv import KVCache, _c_int, _elsewhere, _stream_on, _table, _vec
+from .kv import KVCache, _c_int, _elsewhere, _rows, _stream_on, _table, _vec
 
 LORA_MAX_BEAMS, LORA_MAX_VOCAB, LORA_FORK_META, LORA_MAX_LAYERS = 64, 1 << 24, 8, 128
 
 __all__ = ["LORA_MAX_BEAMS", "LORA_MAX_VOCAB", "LORA_FORK_META", "LORA_MAX_LAYERS", "Beams", "ForkPlan", "KVLayers",
-           "beam_select", "page_fork", "page_copy"]
+           "SharedAttention", "beam_select", "page_fork", "page_copy", "shared_attention"]
 
 
 def _floats(t, least: int, what: str) -> int:
@@ -189,3 +192,65 @@ def page_copy(caches, src, dst, tokens=None, stream=None) -> None:
     if src.get_device() != dev or dst.get_device() != dev or (tokens is not None and tokens.get_device() != dev):
         _elsewhere(dev, ("src", src), ("dst", dst), *([("tokens", tokens)] if tokens is not None else []))
     _check(lib.lora_page_copy(dev, layers, count, s or None, d or None, t or None, n, _stream_on(dev, stream)), "lora_page_copy")
+
+
+class SharedAttention:
+    """Attention over common pages of up to max_seqs sequences and max_tokens new tokens (owns its workspace)."""
+
+    def __init__(self, device: int, max_seqs: int, max_tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int):
+        self.handle = 0
+        for value, what in ((max_seqs, "max_seqs"), (max_tokens, "max_tokens"), (num_q_heads, "num_q_heads"),
+                            (num_kv_heads, "num_kv_heads"), (head_dim, "head_dim")):
+            _c_int(value, what)
+        self.device, self.max_seqs, self.max_tokens = device, max_seqs, max_tokens
+        self.num_q_heads, self.num_kv_heads, self.head_dim = num_q_heads, num_kv_heads, head_dim
+        h = C.c_void_p()
+        _check(lib.lora_shared_create(C.byref(h), device, max_seqs, max_tokens, num_q_heads, num_kv_heads, head_dim),
+               "lora_shared_create")
+        self.handle = h.value
+
+    def close(self) -> None:
+        if self.handle:
+            _check(lib.lora_shared_destroy(self.handle), "lora_shared_destroy")
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def shared_attention(attention: SharedAttention, q, cache: KVCache, block_table, seq_lens, query_start, group_start, common_lens, out,
+                     scale: Optional[float] = None, lse=None, stream=None) -> None:
+    """paged_attention of sequences whose first tokens lie in common pages, which are read once for all of a group (see
+    lora_shared_attention).  group_start: int32 [groups + 1], the first sequence of each group; common_lens: int32
+    [groups], the tokens that its sequences have in common.  The other arguments are paged_attention's."""
+    if kv.torch is None:
+        kv._load()
+    dev = attention.device
+    n = query_start.numel() - 1 if hasattr(query_start, "numel") else 0
+    groups = group_start.numel() - 1 if hasattr(group_start, "numel") else 0
+    starts, lens = _vec(query_start, 1, "query_start"), _vec(seq_lens, n, "seq_lens")
+    first, common = _vec(group_start, 1, "group_start"), _vec(common_lens, groups, "common_lens")
+    if common_lens.numel() != groups:
+        raise ValueError("group_start must have one entry more than common_lens")
+    table, ld, cols = _table(block_table, n)
+    T = q.shape[0] if hasattr(q, "shape") and len(q.shape) else 0
+    width = attention.num_q_heads * attention.head_dim
+    qp, ldq = _rows(q, cache.act, T, width, "q")
+    op, ldo = _rows(out, cache.act, T, width, "out")
+    lp = None
+    if lse is not None:
+        if lse.dtype is not kv.torch.float32 or lse.shape != (T, attention.num_q_heads) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape ({T}, {attention.num_q_heads})")
+        if lse.get_device() != dev:
+            _elsewhere(dev, ("lse", lse))
+        lp = lse.data_ptr()
+    if (q.get_device() != dev or out.get_device() != dev or block_table.get_device() != dev or seq_lens.get_device() != dev or
+            query_start.get_device() != dev or group_start.get_device() != dev or common_lens.get_device() != dev or cache.device != dev):
+        _elsewhere(dev, ("q", q), ("out", out), ("block_table", block_table), ("seq_lens", seq_lens), ("query_start", query_start),
+                   ("group_start", group_start), ("common_lens", common_lens), ("the cache", cache.k))
+    _check(lib.lora_shared_attention(attention.handle, qp or None, ldq, cache.act_code, cache.ref, table, ld, cols, lens, starts, n, T,
+                                         first, common or None, groups, 1.0 / math.sqrt(attention.head_dim) if scale is None else scale,
+                                         op or None, ldo, lp or None, _stream_on(dev, stream)), "lora_shared_attention")
