@@ -582,9 +582,11 @@ __device__ __forceinline__ void attend_shares(const AttentionArgs& a, const Line
       page_of(t, page);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const int row = wrow0 + rt * 16 + c16;
+        // A row that is not there stands for the block's first, without a branch: where lanes part, the compiler
+        // may copy registers that live on (the accumulators of the part before, above 128 dims) before they are together again.
         const bool there = rt * 16 + c16 < wrows;
-        const int i = there ? fast_quot(row, a.group) : 0, h = there ? p.kh * group + row - i * group : 0;
+        const int row = there ? wrow0 + rt * 16 + c16 : p.row0;
+        const int i = fast_quot(row, a.group), h = p.kh * group + row - i * group;
         const KeyRange k = line.keys(r, i, s);
         lo[rt] = there ? k.lo : 0;
         hi[rt] = there ? k.hi : 0;

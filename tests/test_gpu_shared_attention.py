@@ -156,7 +156,9 @@ LARGE = {"one-group": ([(5000, [1 + 37 * i % 700 for i in range(40)])], 1, 32, 8
          "drafts": ([(1000, [300] * 16), (500, [20] * 10)], 4, 16, 2, 128),
          "prompts": ([(700, [300, 260, 400]), (64, [200])], [250, 260, 300, 130], 8, 2, 64),
          "many": ([(64 + 16 * (g % 5), [1 + (i + g) % 40 for i in range(1 + g % 7)]) for g in range(500)], 1, 4, 1, 64),
-         "wide-heads": ([(2000, [60] * 30)], 1, 8, 2, 256), "one-head": ([(9000, [100] * 200)], 1, 8, 1, 96)}
+         "wide-heads": ([(2000, [60] * 30)], 1, 8, 2, 256), "wide-blocks": ([(704, [3] * 107)], 1, 1, 1, 192),
+         "wide-short-blocks": ([(64, [22] * 20)], 1, 32, 4, 256), "wide-drafts": ([(64, [22] * 5), (30, [9] * 9)], 4, 32, 4, 192),
+"one-head": ([(9000, [100] * 200)], 1, 8, 1, 96)}
 
 
 @pytest.mark.parametrize("cache", CACHES)
