@@ -86,22 +86,34 @@ template <> struct Chunk<float> {
   __device__ __forceinline__ static float at(const uint4& c, int e) { return __uint_as_float((&c.x)[e]); }
 };
 
-// Cut a wave's list of n entries back to its `best` largest, in order; returns their number.
+// Numbers of list[0..n) that are above `mine`, kAhead at a time (the loads of a step are on the way together);
+// list[n..) up to the next multiple of kAhead holds zeros.
+constexpr int kAhead = 8;
+__device__ __forceinline__ int above(const u64* list, int n, u64 mine) {
+  int place = 0;
+  for (int j = 0; j < n; j += kAhead) {
+    ulonglong2 two[kAhead / 2];
+#pragma unroll
+    for (int k = 0; k < kAhead / 2; ++k) two[k] = *reinterpret_cast<const ulonglong2*>(list + j + 2 * k);
+#pragma unroll
+    for (int k = 0; k < kAhead / 2; ++k) place += (two[k].x > mine) + (two[k].y > mine);
+  }
+  return place;
+}
+
+// Cut a wave's list of n entries back to its `best` largest, in order, with zeros behind them; returns their number.
 __device__ __forceinline__ int cut_list(u64* list, u64* sorted, int n, int best, int lane) {
-  if (lane == 0) list[n] = 0;   // entries are read two at a time
+  if (lane < kAhead) list[n + lane] = 0;
   wave_lds_sync();
   for (int i = lane; i < n; i += 64) {
     const u64 mine = list[i];
-    int place = 0;
-    for (int j = 0; j < n; j += 2) {
-      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(list + j);
-      place += (two.x > mine) + (two.y > mine);
-    }
+    const int place = above(list, n, mine);
     if (place < best) sorted[place] = mine;
   }
   wave_lds_sync();
   n = min(n, best);
   if (lane < n) list[lane] = sorted[lane];
+  if (lane < kAhead) list[n + lane] = 0;
   wave_lds_sync();
   return n;
 }
@@ -112,7 +124,7 @@ template <typename T>
 __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   using C = Chunk<T>;
   constexpr int N = C::kN, U = kBeamLoads;
-  __shared__ __attribute__((aligned(16))) u64 lists[kBeamWaves][kListCap + 2 + LORA_MAX_BEAMS];
+  __shared__ __attribute__((aligned(16))) u64 lists[kBeamWaves][kListCap + kAhead + LORA_MAX_BEAMS];
   __shared__ double wave_sums[kBeamWaves][2], lse_s[LORA_MAX_BEAMS];
   __shared__ int counts[kBeamWaves], last_s, count_s;
   const int tid = threadIdx.x, lane = lane_id(), w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -151,7 +163,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   const float score = a.scores[row];
   const bool live = score > -INFINITY && !(a.ended && a.ended[row]);   // else the row is not read
   if (live) {
-    u64 *list = lists[w], *sorted = list + kListCap + 2;
+    u64 *list = lists[w], *sorted = list + kListCap + kAhead;
     float m = -INFINITY, l = 0.f, floor_ = -FLT_MAX;
     int n = 0;
     for (bool first = true; tile < tiles; tile += stride, first = false) {
@@ -218,10 +230,9 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     for (int v = 0; v < kBeamWaves; ++v) total += counts[v];
     if (lane < n) {
       const u64 mine = list[lane];
-      int place = 0;
+      int place = lane;
 #pragma unroll
-      for (int v = 0; v < kBeamWaves; ++v)
-        for (int j = 0; j < counts[v]; ++j) place += lists[v][j] > mine;
+      for (int v = 1; v < kBeamWaves; ++v) place += above(lists[(w + v) % kBeamWaves], counts[(w + v) % kBeamWaves], mine);
       if (place < best) put_word(out + place, mine);
     }
     if (tid >= total && tid < best) put_word(out + tid, 0);
@@ -242,7 +253,6 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   if (tid == 0) {
     last_s = __hip_atomic_fetch_add(&a.arrived[request], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.beams * a.segs - 1;
     if (last_s) __hip_atomic_store(&a.arrived[request], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    count_s = 0;
   }
   __syncthreads();
   if (!last_s) return;
@@ -250,13 +260,27 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   // ---- the request's join
   __shared__ float score_s[LORA_MAX_BEAMS], weight_s[LORA_MAX_BEAMS];
   __shared__ int over_s[LORA_MAX_BEAMS];   // 0: read, 1: ended, 2: gives no candidate
-  Entry *entries = reinterpret_cast<Entry*>(&lists[0][0]), *sorted = entries + kListCap;
-  const int row0 = request * a.beams;
-  if (tid < a.beams) {
-    const float c = a.scores[row0 + tid], q = a.weights ? a.weights[row0 + tid] : 1.f;
-    score_s[tid] = c;
-    weight_s[tid] = q;
-    over_s[tid] = !(c > -INFINITY) || !(q > 0.f) ? 2 : a.ended && a.ended[row0 + tid] ? 1 : 0;
+  __shared__ uint32_t floors_s[kBeamWaves];
+  Entry *entries = reinterpret_cast<Entry*>(&lists[0][0]), *sorted = entries + kListCap + kAhead;
+  const int row0 = request * a.beams, per_row = a.segs * best, n = a.beams * per_row;
+  const auto fetch = [&](int i) { return i < n ? get_word(a.keys + (size_t)row0 * per_row + i) : 0; };
+  u64 key = fetch(tid);   // of a row that was not read: what an earlier call left, and not taken
+  if (w == 0) {
+    int over = 2;
+    if (lane < a.beams) {
+      const float c = a.scores[row0 + lane], q = a.weights ? a.weights[row0 + lane] : 1.f;
+      over = !(c > -INFINITY) || !(q > 0.f) ? 2 : a.ended && a.ended[row0 + lane] ? 1 : 0;
+      score_s[lane] = c;
+      weight_s[lane] = q;
+      over_s[lane] = over;
+    }
+    // ended beams
+    const u64 mask = __ballot(over == 1);
+    if (over == 1) {
+      const double r = (double)score_s[lane] * (double)weight_s[lane];
+      entries[__popcll(mask & ((1ull << lane) - 1ull))] = Entry{r, key_of(lane, 0.f, a.end_token)};
+    }
+    if (lane == 0) count_s = __popcll(mask);
   }
   __syncthreads();
   for (int j = w; j < a.beams; j += kBeamWaves) {
@@ -277,28 +301,26 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     if (lane == 0) lse_s[j] = top + log(jl);   // no finite logit, or one that is NaN or +inf: not a number, no candidate
   }
   __syncthreads();
-  const auto candidate = [&](u64 key) {
-    const int j = key_row(key);
-    return over_s[j] == 1 ? (double)score_s[j] : (double)score_s[j] + ((double)key_value(key) - lse_s[j]);
+  const auto candidate = [&](u64 k) {
+    const int j = key_row(k);
+    return over_s[j] == 1 ? (double)score_s[j] : (double)score_s[j] + ((double)key_value(k) - lse_s[j]);
   };
-  const int per_row = a.segs * best, n = a.beams * per_row;
   Entry floor_{-INFINITY, 0};
   bool full = false;
-  // ended beams are candidates of the first round, in place of a list
-  for (int i0 = -kBeamThreads; i0 < n; i0 += kBeamThreads) {
-    u64 key = 0;
-    if (i0 < 0) {
-      if (tid < a.beams && over_s[tid] == 1) key = key_of(tid, 0.f, a.end_token);
-    } else if (i0 + tid < n) {
-      const int j = (int)((unsigned)(i0 + tid) / (unsigned)per_row);
-      if (over_s[j] == 0) key = get_word(a.keys + (size_t)row0 * per_row + i0 + tid);
-    }
-    Entry e{0.0, key};
+  for (int i0 = 0; i0 < n; i0 += kBeamThreads) {
+    const u64 next = fetch(i0 + kBeamThreads + tid);
+    Entry e{-INFINITY, key};
     bool hit = false;
-    if (key) {
+    if (key != 0 && over_s[(unsigned)(i0 + tid) / (unsigned)per_row] == 0) {
       const double s = candidate(key);
       e.rank = s * (double)weight_s[key_row(key)];
       hit = s > -INFINITY && e.rank == e.rank && (!full || e.rank > floor_.rank || (e.rank == floor_.rank && key > floor_.key));
+    }
+    if (i0 == 0) {   // the largest best-th rank of the four waves, rounded down, is a floor
+      const uint32_t mine = hit ? ordered(__double2float_rd(e.rank)) : 0u, least = nth_of_lanes(mine, best);
+      if (lane == 0) floors_s[w] = least;
+      __syncthreads();
+      hit = hit && mine >= max(max(floors_s[0], floors_s[1]), max(floors_s[2], floors_s[3]));
     }
     const u64 mask = __ballot(hit);
     int at = 0;
@@ -307,14 +329,18 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     if (hit) entries[at] = e;
     __syncthreads();
     const int c = count_s;
-    const bool end = i0 + kBeamThreads >= n;
-    if (c > kListCap - kBeamThreads || (end && c > 0)) {
+    if (c > kListCap - kBeamThreads || i0 + kBeamThreads >= n) {
+      if (tid < kAhead) entries[c + tid] = Entry{-INFINITY, 0};   // below every other
+      __syncthreads();
       for (int i = tid; i < c; i += kBeamThreads) {
         const Entry mine = entries[i];
         int place = 0;
-        for (int j = 0; j < c; ++j) {
-          const Entry o = entries[j];
-          place += o.rank > mine.rank || (o.rank == mine.rank && o.key > mine.key);
+        for (int j = 0; j < c; j += kAhead) {
+          Entry o[kAhead];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) o[k] = entries[j + k];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) place += o[k].rank > mine.rank || (o[k].rank == mine.rank && o[k].key > mine.key);
         }
         if (place < best) sorted[place] = mine;
       }
@@ -325,6 +351,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
       full = kept == best;
       if (full) floor_ = sorted[best - 1];
     }
+    key = next;
     __syncthreads();   // the count is read before the next round adds to it
   }
   const int found = count_s;
