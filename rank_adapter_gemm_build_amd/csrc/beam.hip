@@ -137,9 +137,15 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   const int shift = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
   const uint4* const chunks = reinterpret_cast<const uint4*>(x - shift);
   const auto load = [&](int tile, uint4 (&c)[U]) {
+    const int first_ = tile * U * 64 * N - shift;   // token of the tile's first value
+    if (first_ >= 0 && first_ + U * 64 * N <= a.vocab) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) c[u] = chunks[(tile * U + u) * 64 + lane];
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int first = ((tile * U + u) * 64 + lane) * N - shift;   // token of the chunk's first value
+      const int first = first_ + (u * 64 + lane) * N;
       c[u] = make_uint4(C::kNone, C::kNone, C::kNone, C::kNone);
       if (first >= 0 && first + N <= a.vocab) {
         c[u] = chunks[(tile * U + u) * 64 + lane];
@@ -261,10 +267,14 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   __shared__ float score_s[LORA_MAX_BEAMS], weight_s[LORA_MAX_BEAMS];
   __shared__ int over_s[LORA_MAX_BEAMS];   // 0: read, 1: ended, 2: gives no candidate
   __shared__ uint32_t floors_s[kBeamWaves];
-  Entry *entries = reinterpret_cast<Entry*>(&lists[0][0]), *sorted = entries + kListCap + kAhead;
+  constexpr int kFetch = 4, kEntries = LORA_MAX_BEAMS * (2 + kFetch * kBeamWaves);   // ended beams, those kept, new ones
+  static_assert(sizeof(Entry) * (kEntries + kAhead + LORA_MAX_BEAMS) <= sizeof(lists), "the lists' LDS holds the join's");
+  Entry *entries = reinterpret_cast<Entry*>(&lists[0][0]), *sorted = entries + kEntries + kAhead;
   const int row0 = request * a.beams, per_row = a.segs * best, n = a.beams * per_row;
   const auto fetch = [&](int i) { return i < n ? get_word(a.keys + (size_t)row0 * per_row + i) : 0; };
-  u64 key = fetch(tid);   // of a row that was not read: what an earlier call left, and not taken
+  u64 key[kFetch];   // of a row that was not read: what an earlier call left, and not taken
+#pragma unroll
+  for (int k = 0; k < kFetch; ++k) key[k] = fetch(k * kBeamThreads + tid);
   if (w == 0) {
     int over = 2;
     if (lane < a.beams) {
@@ -305,54 +315,60 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     const int j = key_row(k);
     return over_s[j] == 1 ? (double)score_s[j] : (double)score_s[j] + ((double)key_value(k) - lse_s[j]);
   };
-  Entry floor_{-INFINITY, 0};
-  bool full = false;
-  for (int i0 = 0; i0 < n; i0 += kBeamThreads) {
-    const u64 next = fetch(i0 + kBeamThreads + tid);
-    Entry e{-INFINITY, key};
-    bool hit = false;
-    if (key != 0 && over_s[(unsigned)(i0 + tid) / (unsigned)per_row] == 0) {
-      const double s = candidate(key);
-      e.rank = s * (double)weight_s[key_row(key)];
-      hit = s > -INFINITY && e.rank == e.rank && (!full || e.rank > floor_.rank || (e.rank == floor_.rank && key > floor_.key));
+  // kFetch candidates a thread and round.  Those of the best-th largest of a wave's lanes' own best and above come on the
+  // list, at most kFetch for each of `best` lanes a wave, and the list is cut back to `best`.
+  for (int i0 = 0; i0 < n; i0 += kFetch * kBeamThreads) {
+    u64 next[kFetch];
+#pragma unroll
+    for (int k = 0; k < kFetch; ++k) next[k] = fetch(i0 + (kFetch + k) * kBeamThreads + tid);
+    Entry e[kFetch];
+    uint32_t down[kFetch], mine = 0;   // ranks rounded down, as ordered integers; 0: no candidate
+#pragma unroll
+    for (int k = 0; k < kFetch; ++k) {
+      e[k] = Entry{-INFINITY, key[k]};
+      down[k] = 0;
+      if (key[k] != 0 && over_s[(unsigned)(i0 + k * kBeamThreads + tid) / (unsigned)per_row] == 0) {
+        const double s = candidate(key[k]);
+        e[k].rank = s * (double)weight_s[key_row(key[k])];
+        if (s > -INFINITY && e[k].rank == e[k].rank) down[k] = ordered(__double2float_rd(e[k].rank));
+      }
+      mine = max(mine, down[k]);
+      key[k] = next[k];
     }
-    if (i0 == 0) {   // the largest best-th rank of the four waves, rounded down, is a floor
-      const uint32_t mine = hit ? ordered(__double2float_rd(e.rank)) : 0u, least = nth_of_lanes(mine, best);
-      if (lane == 0) floors_s[w] = least;
-      __syncthreads();
-      hit = hit && mine >= max(max(floors_s[0], floors_s[1]), max(floors_s[2], floors_s[3]));
+    const uint32_t least = nth_of_lanes(mine, best);
+    if (lane == 0) floors_s[w] = least;
+    __syncthreads();
+    const uint32_t floor_ = max(max(max(floors_s[0], floors_s[1]), max(floors_s[2], floors_s[3])), 1u);
+#pragma unroll
+    for (int k = 0; k < kFetch; ++k) {
+      const u64 mask = __ballot(down[k] >= floor_);
+      if (mask == 0) continue;
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&count_s, __popcll(mask));
+      at = __shfl(at, 0) + __popcll(mask & ((1ull << lane) - 1ull));
+      if (down[k] >= floor_) entries[at] = e[k];
     }
-    const u64 mask = __ballot(hit);
-    int at = 0;
-    if (lane == 0 && mask) at = atomicAdd(&count_s, __popcll(mask));
-    at = __shfl(at, 0) + __popcll(mask & ((1ull << lane) - 1ull));
-    if (hit) entries[at] = e;
     __syncthreads();
     const int c = count_s;
-    if (c > kListCap - kBeamThreads || i0 + kBeamThreads >= n) {
-      if (tid < kAhead) entries[c + tid] = Entry{-INFINITY, 0};   // below every other
-      __syncthreads();
-      for (int i = tid; i < c; i += kBeamThreads) {
-        const Entry mine = entries[i];
-        int place = 0;
-        for (int j = 0; j < c; j += kAhead) {
-          Entry o[kAhead];
+    if (tid < kAhead) entries[c + tid] = Entry{-INFINITY, 0};   // below every other
+    __syncthreads();
+    for (int i = tid; i < c; i += kBeamThreads) {
+      const Entry own = entries[i];
+      int place = 0;
+      for (int j = 0; j < c; j += kAhead) {
+        Entry o[kAhead];
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) o[k] = entries[j + k];
+        for (int k = 0; k < kAhead; ++k) o[k] = entries[j + k];
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) place += o[k].rank > mine.rank || (o[k].rank == mine.rank && o[k].key > mine.key);
-        }
-        if (place < best) sorted[place] = mine;
+        for (int k = 0; k < kAhead; ++k) place += o[k].rank > own.rank || (o[k].rank == own.rank && o[k].key > own.key);
       }
-      __syncthreads();
-      const int kept = min(c, best);
-      if (tid < kept) entries[tid] = sorted[tid];
-      if (tid == 0) count_s = kept;
-      full = kept == best;
-      if (full) floor_ = sorted[best - 1];
+      if (place < best) sorted[place] = own;
     }
-    key = next;
-    __syncthreads();   // the count is read before the next round adds to it
+    __syncthreads();
+    const int kept = min(c, best);
+    if (tid < kept) entries[tid] = sorted[tid];
+    if (tid == 0) count_s = kept;
+    __syncthreads();
   }
   const int found = count_s;
   if (tid < best) {
