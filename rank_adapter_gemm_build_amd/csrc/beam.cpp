@@ -22,7 +22,7 @@ using rax::timer_for;
 struct lora_beams {
   int device = 0, max_requests = 0, beams = 0, vocab = 0, candidates = 0;
   unsigned long long* keys = nullptr;   // device
-  double* sums = nullptr;               // device
+  unsigned long long* sums = nullptr;   // device
   int* arrived = nullptr;               // device, zero between calls
 };
 
@@ -70,7 +70,7 @@ lora_status lora_beams_create(lora_beams** out, int device, int max_requests, in
     for (int size = 2; size <= 4; size += 2)
       shares = std::max(shares, (size_t)(n * beams) * (size_t)rax::beam_segs(n * beams, vocab, size));
   hipError_t e = hipMalloc(reinterpret_cast<void**>(&b->keys), shares * candidates * sizeof(unsigned long long));
-  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&b->sums), shares * 2 * sizeof(double));
+  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&b->sums), shares * rax::kBeamWaves * 2 * sizeof(unsigned long long));
   if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&b->arrived), max_requests * sizeof(int));
   if (e == hipSuccess) e = hipMemset(b->arrived, 0, max_requests * sizeof(int));
   if (e == hipSuccess) e = hipDeviceSynchronize();

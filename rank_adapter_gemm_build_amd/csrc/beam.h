@@ -21,7 +21,7 @@ struct BeamArgs {
   // the launch's shape and workspace
   int segs;                        // workgroups of a row
   unsigned long long* keys;        // [rows][segs][best]
-  double* sums;                    // [rows][segs][2]
+  unsigned long long* sums;        // [rows][segs * kBeamWaves][2]: maximum (fp32) and sum (fp64) of a wave
   int* arrived;                    // [requests], zero between launches
 };
 constexpr int kBeamWaves = 4, kBeamLoads = 4;                  // waves of a workgroup; 16-byte loads of a lane and tile

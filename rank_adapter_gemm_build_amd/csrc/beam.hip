@@ -57,8 +57,34 @@ __device__ __forceinline__ int key_row(u64 key) { return 63 - (int)(key >> 56); 
 
 __device__ __forceinline__ u64 get_word(const u64* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ void put_word(u64* p, u64 v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-__device__ __forceinline__ double get_double(const double* p) { return __longlong_as_double((long long)get_word(reinterpret_cast<const u64*>(p))); }
-__device__ __forceinline__ void put_double(double* p, double v) { put_word(reinterpret_cast<u64*>(p), (u64)__double_as_longlong(v)); }
+
+// Maximum, and sum in 64 bits, over the wave by lane moves (row_shr 1, 2, 4, 8, row_bcast 15 and 31), in every lane
+template <int CTRL, int ROWS> __device__ __forceinline__ float max_step(float v) {
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(-INFINITY), __float_as_int(v), CTRL, ROWS, 0xf, false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = max_step<0x118, 0xf>(max_step<0x114, 0xf>(max_step<0x112, 0xf>(max_step<0x111, 0xf>(v))));
+  v = max_step<0x143, 0xc>(max_step<0x142, 0xa>(v));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ double sum_step(double v) {
+  const u64 u = (u64)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+  return v + __longlong_as_double((long long)((u64)hi << 32 | lo));
+}
+__device__ __forceinline__ double wave_sum64(double v) {
+  v = sum_step<0x118, 0xf>(sum_step<0x114, 0xf>(sum_step<0x112, 0xf>(sum_step<0x111, 0xf>(v))));
+  v = sum_step<0x143, 0xc>(sum_step<0x142, 0xa>(v));
+  const u64 u = (u64)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __longlong_as_double((long long)((u64)hi << 32 | lo));
+}
+// sum of the lanes' l at maxima m, relative to the largest maximum
+__device__ __forceinline__ double joined_sum(float m, double l, float& top) {
+  top = wave_max(m);
+  return wave_sum64(m == top ? l : l * exp((double)m - (double)top));   // m = -inf: 0
+}
 
 // the n-th largest of the lanes' keys, 0 if n is above 64
 __device__ __forceinline__ uint32_t nth_of_lanes(uint32_t key, int n) {
@@ -125,7 +151,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   using C = Chunk<T>;
   constexpr int N = C::kN, U = kBeamLoads;
   __shared__ __attribute__((aligned(16))) u64 lists[kBeamWaves][kListCap + kAhead + LORA_MAX_BEAMS];
-  __shared__ double wave_sums[kBeamWaves][2], lse_s[LORA_MAX_BEAMS];
+  __shared__ double lse_s[LORA_MAX_BEAMS];
   __shared__ int counts[kBeamWaves], last_s, count_s;
   const int tid = threadIdx.x, lane = lane_id(), w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs, request = row / a.beams, beam = row - request * a.beams;
@@ -163,11 +189,21 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     }
   };
   const int tile_n = 64 * U * N, tiles = (a.vocab + shift + tile_n - 1) / tile_n, stride = a.segs * kBeamWaves;
-  int tile = seg * kBeamWaves + w;
+  const int tile0 = seg * kBeamWaves + w;   // this wave among the row's
+  int tile = tile0;
   uint4 cur[U], nxt[U];
+  // the request's beams, one a lane (over: 0 read, 1 ended, 2 without a candidate)
+  float lane_score = -INFINITY, lane_weight = 1.f;
+  int over = 2;
+  if (lane < a.beams) {
+    const int r = request * a.beams + lane;
+    lane_score = a.scores[r];
+    if (a.weights) lane_weight = a.weights[r];
+    over = a.ended ? a.ended[r] : 0;
+  }
   load(tile, cur);
-  const float score = a.scores[row];
-  const bool live = score > -INFINITY && !(a.ended && a.ended[row]);   // else the row is not read
+  over = !(lane_score > -INFINITY) || !(lane_weight > 0.f) ? 2 : over != 0;
+  const bool live = __builtin_amdgcn_readlane(over, beam) == 0;   // else the row is not read
   if (live) {
     u64 *list = lists[w], *sorted = list + kListCap + kAhead;
     float m = -INFINITY, l = 0.f, floor_ = -FLT_MAX;
@@ -217,19 +253,15 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     }
     n = cut_list(list, sorted, n, best, lane);
     // the wave's sum
-    float wm = m;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) wm = fmaxf(wm, __shfl_xor(wm, d));
-    double wl = (double)l * (m == wm ? 1.0 : exp((double)m - (double)wm));   // m = -inf: 0
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) wl += __shfl_xor(wl, d);
+    float top;
+    const double sum = joined_sum(m, (double)l, top);
     if (lane == 0) {
       counts[w] = n;
-      wave_sums[w][0] = wm;
-      wave_sums[w][1] = wl;
+      put_word(a.sums + 2 * ((size_t)row * stride + tile0), (u64)__float_as_uint(top));
+      put_word(a.sums + 2 * ((size_t)row * stride + tile0) + 1, (u64)__double_as_longlong(sum));
     }
     __syncthreads();
-    // the workgroup's list and sum
+    // the workgroup's list
     u64* out = a.keys + ((size_t)row * a.segs + seg) * best;
     int total = 0;
 #pragma unroll
@@ -242,17 +274,6 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
       if (place < best) put_word(out + place, mine);
     }
     if (tid >= total && tid < best) put_word(out + tid, 0);
-    if (tid == 0) {
-      double gm = wave_sums[0][0], gl = 0.0;
-#pragma unroll
-      for (int v = 1; v < kBeamWaves; ++v) gm = fmax(gm, wave_sums[v][0]);
-#pragma unroll
-      for (int v = 0; v < kBeamWaves; ++v)
-        gl += wave_sums[v][1] * (wave_sums[v][0] == gm ? 1.0 : exp(wave_sums[v][0] - gm));
-      double* s = a.sums + ((size_t)row * a.segs + seg) * 2;
-      put_double(s, gm);
-      put_double(s + 1, gl);
-    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // every store of this wave has arrived
   }
   __syncthreads();
@@ -275,40 +296,47 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   u64 key[kFetch];   // of a row that was not read: what an earlier call left, and not taken
 #pragma unroll
   for (int k = 0; k < kFetch; ++k) key[k] = fetch(k * kBeamThreads + tid);
+  // the rows' log sums, kRows of a wave's at a time
+  constexpr int kRows = 4;
+  const int parts = a.segs * kBeamWaves;
+  for (int j0 = w; j0 < a.beams; j0 += kRows * kBeamWaves) {
+    float m[kRows];
+    double l[kRows];
+    const auto part = [&](int j, int i, float& pm, double& pl) {
+      const u64* p = a.sums + 2 * ((size_t)(row0 + j) * parts + i);
+      pm = i < parts ? __uint_as_float((uint32_t)get_word(p)) : -INFINITY;
+      pl = i < parts ? __longlong_as_double((long long)get_word(p + 1)) : 0.0;
+    };
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (j0 + k * kBeamWaves < a.beams) part(j0 + k * kBeamWaves, lane, m[k], l[k]);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int j = j0 + k * kBeamWaves;
+      if (j >= a.beams || __builtin_amdgcn_readlane(over, j) != 0) continue;
+      for (int i = 64 + lane; i - lane < parts; i += 64) {
+        float pm;
+        double pl;
+        part(j, i, pm, pl);
+        const float nm = fmaxf(m[k], pm);
+        l[k] = (m[k] == nm ? l[k] : l[k] * exp((double)m[k] - (double)nm)) + (pm == nm ? pl : pl * exp((double)pm - (double)nm));
+        m[k] = nm;
+      }
+      float top;
+      const double sum = joined_sum(m[k], l[k], top);
+      if (lane == 0) lse_s[j] = (double)top + log(sum);   // no finite logit, or one that is NaN or +inf: not a number, no candidate
+    }
+  }
   if (w == 0) {
-    int over = 2;
     if (lane < a.beams) {
-      const float c = a.scores[row0 + lane], q = a.weights ? a.weights[row0 + lane] : 1.f;
-      over = !(c > -INFINITY) || !(q > 0.f) ? 2 : a.ended && a.ended[row0 + lane] ? 1 : 0;
-      score_s[lane] = c;
-      weight_s[lane] = q;
+      score_s[lane] = lane_score;
+      weight_s[lane] = lane_weight;
       over_s[lane] = over;
     }
     // ended beams
     const u64 mask = __ballot(over == 1);
-    if (over == 1) {
-      const double r = (double)score_s[lane] * (double)weight_s[lane];
-      entries[__popcll(mask & ((1ull << lane) - 1ull))] = Entry{r, key_of(lane, 0.f, a.end_token)};
-    }
+    if (over == 1) entries[__popcll(mask & ((1ull << lane) - 1ull))] = Entry{(double)lane_score * (double)lane_weight, key_of(lane, 0.f, a.end_token)};
     if (lane == 0) count_s = __popcll(mask);
-  }
-  __syncthreads();
-  for (int j = w; j < a.beams; j += kBeamWaves) {
-    if (over_s[j]) continue;
-    const double* s = a.sums + (size_t)(row0 + j) * a.segs * 2;
-    double jm = -INFINITY, jl = 0.0;
-    for (int i = lane; i < a.segs; i += 64) {
-      const double pm = get_double(s + 2 * i), pl = get_double(s + 2 * i + 1), nm = fmax(jm, pm);
-      jl = jl * (jm == nm ? 1.0 : exp(jm - nm)) + pl * (pm == nm ? 1.0 : exp(pm - nm));
-      jm = nm;
-    }
-    double top = jm;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d));
-    jl *= jm == top ? 1.0 : exp(jm - top);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) jl += __shfl_xor(jl, d);
-    if (lane == 0) lse_s[j] = top + log(jl);   // no finite logit, or one that is NaN or +inf: not a number, no candidate
   }
   __syncthreads();
   const auto candidate = [&](u64 k) {
