@@ -36,7 +36,6 @@ struct PageForkArgs {
   int32_t *lens, *ring, *cursor, *shares, *table, *copy_src, *copy_dst, *copy_tokens, *meta;
   uint32_t* freed;                 // [(num_pages + 31) / 32], zero between launches
   int rows, page_shift, num_pages, ld_table, max_pages;
-  int columns;                     // of a strip (a power of two), set by the launcher
 };
 hipError_t launch_page_fork(const PageForkArgs& a, hipStream_t stream, const KTimer& tm);
 

@@ -33,13 +33,13 @@ RAX_HD int holders_change(RowPages p, int c, int children) {
   return c == p.full && p.part > 0 && children == 0 ? -1 : 0;
 }
 
-// Columns of a strip: a workgroup takes a strip of all rows, kForkPer entries a thread, and at least
-// one 64-byte piece of a row where the rows allow it.
-constexpr int kForkThreads = 1024, kForkPer = 16, kForkMaxColumns = 64;
-inline int fork_columns(int rows) {
-  int c = kForkMaxColumns;
-  while (c > 1 && (long long)c * rows > (long long)kForkThreads * kForkPer) c /= 2;
-  return c;
+// Columns of a strip (a workgroup takes a strip of all rows), and the strip of a workgroup of `strips` ones: strips that
+// share cache lines on one die.
+constexpr int kForkColumns = 4;
+RAX_HD int strip_of_block(int block, int strips) {
+  const int per = (strips + kDies - 1) / kDies, place = block / kDies;
+  const int s = place < per ? block % kDies * per + place : strips;
+  return s < strips ? s : strips;
 }
 
 }  // namespace rax

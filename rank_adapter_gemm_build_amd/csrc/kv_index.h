@@ -132,6 +132,7 @@ inline int attention_workers(int cus) {
   const int w = 2 * cus / (2 * kDies) * (2 * kDies);
   return w < 2 * kDies ? 2 * kDies : (w > 512 ? 512 : w);
 }
+RAX_HD int whole_dies(int n) { return (n + kDies - 1) / kDies * kDies; }
 // The share of workgroup `block`, or `workers` if it has none: neighbouring shares on one die (the
 // row blocks of a head read its keys from one L2), and as many on each.
 RAX_HD int share_of_block(int block, int workers) {

@@ -7,11 +7,13 @@
 // gets a bit in `freed`; at the end the bits, in order of the page ids, follow the ring's free pages.
 // So the result does not depend on the order of the atomics.
 //
-// What bounds it: latency, a chain of loads (parents and lengths, table, counts), two scans and
+// What bounds it: latency, a chain of loads (parents and lengths, table, counts), a scan and
 // the hand-over to the workgroup that finishes last.  Table columns are independent of each
-// other, so a workgroup takes a strip of columns of all rows: it reads the entries of its new rows
-// into registers, and writes them after a barrier, which makes the call work in place.  Every
-// workgroup scans the rows by itself.  The workgroup that finishes last writes what the others
+// other, so a workgroup takes a strip of kForkColumns of all rows, a lane a row: the old entries go to
+// LDS, where the new rows find them after a barrier, which makes the call work in place.  Beams lie
+// side by side and hold mostly the same pages: the changes of a run of lanes with one page are
+// summed first, and for pages that all beams of a request hold come to nothing, which leaves few atomics.
+// Every workgroup scans the rows by itself.  The one that finishes last writes what the others
 // had to read: lengths, ring, cursor.
 #include <hip/hip_runtime.h>
 
@@ -26,14 +28,12 @@ namespace rax {
 
 namespace {
 
-constexpr int kForkWaves = kForkThreads / 64, kForkRows = LORA_MAX_SEQS / kForkThreads;   // rows of a thread
-
 __device__ __forceinline__ int atomic_add_agent(int* p, int v) {
   return __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// exclusive sum over the workgroup's threads, and the total (capped)
-__device__ __forceinline__ int block_scan(int x, int* part, int tid, int& total) {
+// Exclusive sum over the workgroup's threads, and the total (capped).  part: LDS, not in use before the barrier in here.
+template <int WAVES> __device__ __forceinline__ int block_scan(int x, int* part, int tid, int& total) {
   const int lane = tid & 63, w = tid >> 6, in = wave_sat_scan(x);
   if (lane == 63) part[w] = in;
   __syncthreads();
@@ -41,73 +41,97 @@ __device__ __forceinline__ int block_scan(int x, int* part, int tid, int& total)
   if (lane == 0) before = 0;
   total = 0;
 #pragma unroll
-  for (int v = 0; v < kForkWaves; ++v) {
+  for (int v = 0; v < WAVES; ++v) {
     if (v < w) before = sat_add(before, part[v]);
     total = sat_add(total, part[v]);
   }
-  __syncthreads();
   return before;
+}
+
+// The sum of `change` over a run of neighbouring lanes with one page, in the run's last lane; 0 in the others.  All lanes active.
+__device__ __forceinline__ int run_sum(int page, int change, int lane) {
+  const int sum = wave_inclusive_scan(change), before = __shfl_up(page, 1), after = __shfl_down(page, 1);
+  const unsigned long long heads = __ballot(lane == 0 || before != page);
+  const int head = 63 - __clzll(heads & (~0ull >> (63 - lane)));
+  const int skip = __shfl(sum, max(head - 1, 0));
+  return lane == 63 || after != page ? sum - (head > 0 ? skip : 0) : 0;
 }
 
 }  // namespace
 
-__global__ __launch_bounds__(kForkThreads) void page_fork_kernel(PageForkArgs a) {
-  // of an old row: its length, its first child, its number of granted children; of a new
-  // one: its parent (-1 if it has none or is refused) and its place among the drawn pages (-1: draws none)
-  extern __shared__ int lds[];
-  __shared__ int part_s[kForkWaves], refused_s, invalid_s, last_s;
-  const int R = a.rows, N = a.num_pages, ps = a.page_shift, tid = threadIdx.x;
-  int *len_s = lds, *first_s = len_s + R, *kids_s = first_s + R, *parent_s = kids_s + R, *draw_s = parent_s + R;
-  const int head = ring_head(a.cursor[0], N), free_pages = clamp_int(a.cursor[1], 0, N);
+// T: threads; PER: rows of a thread
+template <int T, int PER> __global__ __launch_bounds__(T) void page_fork_kernel(PageForkArgs a) {
+  constexpr int C = kForkColumns, W = T / 64;
+  // of an old row: its entries in the strip, its length, its first child, its number of granted children
+  extern __shared__ int4 strip_s[];
+  __shared__ int part_s[2][W], refused_s, invalid_s, last_s;
+  const int R = a.rows, N = a.num_pages, ps = a.page_shift, tid = threadIdx.x, lane = tid & 63;
+  int *len_s = reinterpret_cast<int*>(strip_s + R), *first_s = len_s + R, *kids_s = first_s + R;
   const bool first_wg = blockIdx.x == 0;
-  if (tid == 0) refused_s = invalid_s = 0;
 
   // ---- rows, a run of consecutive ones for each thread
-  const int per = (R + kForkThreads - 1) / kForkThreads, r0 = min(R, tid * per), count = min(R, r0 + per) - r0;
-  int parent[kForkRows], invalid = 0;
+  const int per = (R + T - 1) / T, r0 = min(R, tid * per), count = min(R, r0 + per) - r0;
+  int parent[PER], len[PER], invalid = 0;
 #pragma unroll
-  for (int i = 0; i < kForkRows; ++i) {
+  for (int i = 0; i < PER; ++i) {
     parent[i] = -1;
+    len[i] = 0;
+    if (i < count) {
+      parent[i] = a.parents[r0 + i];
+      len[i] = a.lens[r0 + i];
+    }
+  }
+  const int head = ring_head(a.cursor[0], N), free_pages = clamp_int(a.cursor[1], 0, N);
+  if (tid == 0) refused_s = invalid_s = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (i < count) {
+      first_s[r0 + i] = R;
+      kids_s[r0 + i] = 0;
+    }
+  int longest = 0;   // pages of the longest row
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
     if (i >= count) continue;
-    const int p = a.parents[r0 + i], len = a.lens[r0 + i];
-    parent[i] = parent_or_none(p, R);
-    const RowPages own = row_pages(len, ps, a.max_pages);
-    if (first_wg) invalid += own.invalid + (p != parent[i] && p != -1);
-    len_s[r0 + i] = own.invalid ? 0 : len;
-    first_s[r0 + i] = R;
-    kids_s[r0 + i] = 0;
+    const int p = parent_or_none(parent[i], R);
+    const RowPages own = row_pages(len[i], ps, a.max_pages);
+    if (first_wg) invalid += own.invalid + (p != parent[i] && parent[i] != -1);
+    parent[i] = p;
+    len[i] = own.invalid ? 0 : len[i];
+    len_s[r0 + i] = len[i];
+    longest = max(longest, own.all());
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kForkRows; ++i)
+  for (int i = 0; i < PER; ++i)
     if (parent[i] >= 0) atomicMin(&first_s[parent[i]], r0 + i);
   __syncthreads();
-  int need = 0;
-  bool draws[kForkRows];
+  int need = 0, draw[PER], size[PER];   // place among the drawn pages (-1: draws none); length of the new row
 #pragma unroll
-  for (int i = 0; i < kForkRows; ++i) {
-    draws[i] = parent[i] >= 0 && first_s[parent[i]] != r0 + i && (len_s[parent[i]] & ((1 << ps) - 1)) > 0;
-    need += draws[i];
+  for (int i = 0; i < PER; ++i) {
+    size[i] = parent[i] >= 0 ? len_s[parent[i]] : 0;
+    draw[i] = parent[i] >= 0 && first_s[parent[i]] != r0 + i && (size[i] & ((1 << ps) - 1)) > 0 ? 0 : -1;
+    need += draw[i] == 0;
   }
-  int needs, refused = 0;
-  int place = block_scan(need, part_s, tid, needs);
+  for (int d = 32; d > 0; d >>= 1) longest = max(longest, __shfl_xor(longest, d));
+  if (lane == 0) part_s[1][tid >> 6] = longest;
+  int needs, refused = 0, place = block_scan<W>(need, part_s[0], tid, needs);
+#pragma unroll
+  for (int v = 0; v < W; ++v) longest = max(longest, part_s[1][v]);
   const int taken = min(needs, free_pages);
 #pragma unroll
-  for (int i = 0; i < kForkRows; ++i) {
-    if (i >= count) continue;
-    int draw = -1;
-    if (draws[i]) {
-      if (place < free_pages) draw = place;
-      else {
+  for (int i = 0; i < PER; ++i) {
+    if (draw[i] == 0) {
+      draw[i] = place < free_pages ? place : -1;
+      if (place >= free_pages) {
         parent[i] = -1;
+        size[i] = 0;
         ++refused;
       }
       ++place;
     }
     if (parent[i] >= 0) atomicAdd(&kids_s[parent[i]], 1);
-    parent_s[r0 + i] = parent[i];
-    draw_s[r0 + i] = draw;
-    if (first_wg && draw < 0) {
+    if (first_wg && i < count && draw[i] < 0) {
       a.copy_src[r0 + i] = a.copy_dst[r0 + i] = -1;
       a.copy_tokens[r0 + i] = 0;
     }
@@ -116,76 +140,116 @@ __global__ __launch_bounds__(kForkThreads) void page_fork_kernel(PageForkArgs a)
   __syncthreads();
 
   // ---- strips of columns
-  const int C = a.columns, shift = 31 - __clz(C), strips = (a.max_pages + C - 1) / C;
-  for (int strip = blockIdx.x; strip < strips; strip += gridDim.x) {
-    const int c0 = strip * C;
-    int id[kForkPer], old[kForkPer];   // entry of the new row, of the old one (-1: none)
-    bool write[kForkPer], holds[kForkPer];
+  const int strips = (longest + C - 1) / C;
+  const bool whole = a.ld_table % 4 == 0 && (reinterpret_cast<uintptr_t>(a.table) & 15u) == 0;   // 16 bytes of a row at a time
+  for (int b = blockIdx.x; b < (strips + kDies - 1) / kDies * kDies; b += gridDim.x) {
+    const int strip = strip_of_block(b, strips), c0 = strip * C;
+    if (strip >= strips) continue;
+    int old[PER][C];
 #pragma unroll
-    for (int k = 0; k < kForkPer; ++k) {
-      const int e = k * kForkThreads + tid, i = e >> shift, c = c0 + (e & (C - 1));
-      write[k] = holds[k] = false;
-      id[k] = old[k] = -1;
-      if (i >= R || c >= a.max_pages) continue;
-      const int p = parent_s[i];
-      write[k] = p >= 0 && c < row_pages(len_s[p], ps, a.max_pages).all();
-      holds[k] = c < row_pages(len_s[i], ps, a.max_pages).all();
-      if (write[k]) id[k] = a.table[(size_t)p * a.ld_table + c];
-      if (holds[k]) old[k] = a.table[(size_t)i * a.ld_table + c];
+    for (int i = 0; i < PER; ++i) {
+      const int used = row_pages(len[i], ps, a.max_pages).all() - c0;   // entries of this row in the strip
+      const int32_t* src = a.table + (size_t)(r0 + i) * a.ld_table + c0;
+#pragma unroll
+      for (int k = 0; k < C; ++k) old[i][k] = -1;
+      if (i >= count || used <= 0) continue;
+      if (whole && c0 + C <= a.max_pages) {
+        const int4 v = *reinterpret_cast<const int4*>(src);
+        old[i][0] = v.x;
+        old[i][1] = used > 1 ? v.y : -1;
+        old[i][2] = used > 2 ? v.z : -1;
+        old[i][3] = used > 3 ? v.w : -1;
+      } else {
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+          if (k < used) old[i][k] = src[k];
+      }
     }
 #pragma unroll
-    for (int k = 0; k < kForkPer; ++k) {   // holders of the old rows' pages
-      const int e = k * kForkThreads + tid, i = e >> shift, c = c0 + (e & (C - 1));
-      if (!holds[k]) continue;
-      const int page = page_or_none(old[k], N), change = holders_change(row_pages(len_s[i], ps, a.max_pages), c, kids_s[i]);
-      invalid += page < 0;
-      old[k] = -1;   // from here on a page that nothing holds any more
-      if (page < 0 || change == 0) continue;
-      const int before = atomic_add_agent(&a.shares[page], change);
-      if (before >= 0 && before + change < 0) old[k] = page;
-    }
+    for (int i = 0; i < PER; ++i) {
+      if (i >= count) continue;
+      const int used = row_pages(len[i], ps, a.max_pages).all() - c0;
 #pragma unroll
-    for (int k = 0; k < kForkPer; ++k) {
-      const int e = k * kForkThreads + tid, i = e >> shift, c = c0 + (e & (C - 1));
-      if (holds[k] && old[k] >= 0)
-        __hip_atomic_fetch_or(&a.freed[old[k] >> 5], 1u << (old[k] & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (!write[k]) continue;
-      id[k] = page_or_none(id[k], N);
-      const RowPages pages = row_pages(len_s[parent_s[i]], ps, a.max_pages);
-      if (c != pages.full || draw_s[i] < 0) continue;
-      const int fresh = page_or_none(a.ring[ring_at(head, draw_s[i], N)], N);   // the new row's own last page
-      invalid += fresh < 0;
-      const bool both = fresh >= 0 && id[k] >= 0;
-      a.copy_src[i] = both ? id[k] : -1;
-      a.copy_dst[i] = both ? fresh : -1;
-      a.copy_tokens[i] = both ? pages.part : 0;
-      id[k] = fresh;
+      for (int k = 0; k < C; ++k) {
+        old[i][k] = page_or_none(old[i][k], N);
+        invalid += k < used && old[i][k] < 0;
+      }
+      strip_s[r0 + i] = make_int4(old[i][0], old[i][1], old[i][2], old[i][3]);
     }
     __syncthreads();   // every entry of the strip has been read
+    // new rows
 #pragma unroll
-    for (int k = 0; k < kForkPer; ++k) {
-      const int e = k * kForkThreads + tid, i = e >> shift, c = c0 + (e & (C - 1));
-      if (write[k]) a.table[(size_t)i * a.ld_table + c] = id[k];
+    for (int i = 0; i < PER; ++i) {
+      const RowPages pages = row_pages(size[i], ps, a.max_pages);
+      const int used = pages.all() - c0;
+      if (i >= count || used <= 0) continue;
+      const int4 v = strip_s[parent[i]];
+      int id[C] = {v.x, v.y, v.z, v.w};
+      if (draw[i] >= 0 && pages.full >= c0 && pages.full < c0 + C) {   // its last page lies here, and is its own
+        const int fresh = page_or_none(a.ring[ring_at(head, draw[i], N)], N);
+        int src = -1;
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+          if (c0 + k == pages.full) {
+            src = id[k];
+            id[k] = fresh;
+          }
+        const bool both = fresh >= 0 && src >= 0;
+        invalid += fresh < 0;
+        a.copy_src[r0 + i] = both ? src : -1;
+        a.copy_dst[r0 + i] = both ? fresh : -1;
+        a.copy_tokens[r0 + i] = both ? pages.part : 0;
+      }
+      int32_t* dst = a.table + (size_t)(r0 + i) * a.ld_table + c0;
+      if (whole && used >= C) *reinterpret_cast<int4*>(dst) = make_int4(id[0], id[1], id[2], id[3]);
+      else {
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+          if (k < used) dst[k] = id[k];
+      }
     }
+    // holders of the old rows' pages.  Lane by lane the rows lie PER apart, so runs are those of every PER-th row.
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const RowPages own = row_pages(len[i], ps, a.max_pages);
+      const int kids = i < count ? kids_s[r0 + i] : 1;
+      int change[C], before[C];
+#pragma unroll
+      for (int k = 0; k < C; ++k) change[k] = run_sum(old[i][k], old[i][k] >= 0 ? holders_change(own, c0 + k, kids) : 0, lane);
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        before[k] = -1;
+        if (change[k] != 0 && old[i][k] >= 0) before[k] = atomic_add_agent(&a.shares[old[i][k]], change[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        if (before[k] >= 0 && before[k] + change[k] < 0)
+          __hip_atomic_fetch_or(&a.freed[old[i][k] >> 5], 1u << (old[i][k] & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();   // the strip's entries in LDS are done with
   }
   if (invalid) atomicAdd(&invalid_s, invalid);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's atomics have arrived
   __syncthreads();
   if (tid == 0) {
-    if (invalid_s) atomic_add_agent(&a.cursor[3], invalid_s);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (invalid_s) {
+      atomic_add_agent(&a.cursor[3], invalid_s);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
     last_s = atomic_add_agent(&a.cursor[2], 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
   if (!last_s) return;
 
   // ---- the last workgroup: lengths, freed pages to the ring's end in order of their ids
-  for (int i = tid; i < R; i += kForkThreads) a.lens[i] = parent_s[i] >= 0 ? len_s[parent_s[i]] : 0;
-  const int words = (N + 31) / 32, run = (words + kForkThreads - 1) / kForkThreads;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (i < count) a.lens[r0 + i] = size[i];
+  const int words = (N + 31) / 32, run = (words + T - 1) / T;
   const int w0 = min(words, tid * run), w1 = min(words, w0 + run);
   int mine = 0, back;
   for (int i = w0; i < w1; ++i) mine += __popc(__hip_atomic_load(&a.freed[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-  int at = block_scan(mine, part_s, tid, back);
+  int at = block_scan<W>(mine, part_s[0], tid, back);
   const int kept = min(back, N - free_pages);   // a ring of N places holds no more
   if (mine > 0)
     for (int i = w0; i < w1; ++i) {
@@ -212,11 +276,11 @@ __global__ __launch_bounds__(kForkThreads) void page_fork_kernel(PageForkArgs a)
   a.meta[5] = a.meta[6] = a.meta[7] = 0;
 }
 
-hipError_t launch_page_fork(const PageForkArgs& given, hipStream_t stream, const KTimer& tm) {
-  PageForkArgs a = given;
-  a.columns = fork_columns(a.rows);
-  const int strips = (a.max_pages + a.columns - 1) / a.columns, wgs = std::min(512, strips);
-  RAX_LAUNCH(tm, page_fork_kernel, dim3(wgs), dim3(kForkThreads), (uint32_t)(5 * sizeof(int) * a.rows), stream, a);
+hipError_t launch_page_fork(const PageForkArgs& a, hipStream_t stream, const KTimer& tm) {
+  const int strips = (a.max_pages + kForkColumns - 1) / kForkColumns, wgs = std::min(256, whole_dies(strips));
+  const uint32_t lds = (uint32_t)(7 * sizeof(int) * a.rows);
+  if (a.rows <= 256) RAX_LAUNCH(tm, (page_fork_kernel<256, 1>), dim3(wgs), dim3(256), lds, stream, a);
+  else RAX_LAUNCH(tm, (page_fork_kernel<1024, LORA_MAX_SEQS / 1024>), dim3(wgs), dim3(1024), lds, stream, a);
   return hipGetLastError();
 }
 

@@ -51,7 +51,7 @@ RAX_HD SeqSpan common_span(const SeqRows& s, int step_log2) {
 struct LineSplit {
   int common, own, own_at;
 };
-RAX_HD int whole_dies(int n) { return (n + kDies - 1) / kDies * kDies; }
+
 RAX_HD LineSplit split_lines(int common_work, int common_min, int own_work, int own_min, int grid) {
   LineSplit s;
   const int c = (int)(((long long)common_work + common_min - 1) / common_min), o = (int)(((long long)own_work + own_min - 1) / own_min);
