@@ -259,6 +259,70 @@ struct PagedLine {
   __device__ __forceinline__ int* arrived() const { return a.arrived; }
 };
 
+// The parts of a unit join in a tree, kJoin at a time: of the workgroups of a node the last to arrive adds their parts,
+// in order, and goes on to the next level with the sum; the one at the root calls finish(row, dim, m, l, o) for 4 dims at
+// a time.  first: the workgroup in which the unit begins; row_sums, last_s: LDS; DB: dims, rounded up as above.
+template <int DB, int kThreads, int kRows, class Line, class Finish>
+__device__ __forceinline__ void join_tree(const AttentionArgs& a, const Line& line, const Part& p, int D, int tid, int b, int first, int work,
+                                          int workers, float2* row_sums, int& last_s, const Finish& finish) {
+  const auto part_o = cells_at(reinterpret_cast<const char*>(line.part_o()), true);   // below 2^31 bytes
+  const auto part_ml = cells_at(reinterpret_cast<const char*>(line.part_ml()), true);
+  auto part_row = [&](int k, int lrow) { return (uint32_t)part_slot(first, k) * (uint32_t)kRows + (uint32_t)lrow; };
+  const int parts = share_owner(work, workers, p.at + p.steps - 1) - first + 1;
+  int k0 = b - first;
+  for (int level = 0, stride = 1; stride < parts; ++level, stride *= kJoin) {
+    k0 -= k0 % (stride * kJoin);
+    const int n = min(kJoin, (parts - k0 + stride - 1) / stride);
+    const bool root = stride * kJoin >= parts;
+    if (n == 1) continue;
+    stores_done();
+    lds_barrier();
+    if (tid == 0) {
+      int* arrived = line.arrived() + level * a.counters + first + k0;
+      last_s = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+      if (last_s) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    lds_barrier();
+    if (!last_s) break;
+    for (int it = tid; it < p.rows * (DB / 4); it += kThreads) {
+      const int lrow = it / (DB / 4), d = it % (DB / 4) * 4;
+      if (d >= D) continue;
+      f32x4_t v[kJoin];
+      float2 x[kJoin];
+#pragma unroll
+      for (int k = 0; k < kJoin; ++k) {
+        const uint32_t at = part_row(k0 + k * stride, lrow);
+        x[k] = get_shared2(part_ml, k < n ? at * 8 : kNowhere);
+        v[k] = get_shared(part_o, k < n ? (at * D + d) * 4 : kNowhere);
+      }
+      float mm = -INFINITY, ll = 0.f;
+      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kJoin; ++k)
+        if (k < n) mm = fmaxf(mm, x[k].x);
+#pragma unroll
+      for (int k = 0; k < kJoin; ++k)
+        if (k < n) {
+          const float f = __builtin_amdgcn_exp2f(x[k].x - finite_top(mm));
+          ll += x[k].y * f;
+          acc += v[k] * f;
+        }
+      if (root) {
+        finish(lrow, d, mm, ll, acc);
+      } else {
+        const uint32_t at = part_row(k0, lrow);
+        put_shared(part_o, (at * D + d) * 4, acc);
+        // the row's other threads still read its sums: they are written after the loop
+        if (d == 0) row_sums[lrow] = make_float2(mm, ll);
+      }
+    }
+    lds_barrier();
+    if (!root)
+      for (int lrow = tid; lrow < p.rows; lrow += kThreads)
+        put_shared2(part_ml, part_row(k0, lrow) * 8, row_sums[lrow].x, row_sums[lrow].y);
+  }
+}
+
 // The shares of a line that this workgroup has: share b_ of workers_ equal ones of the line's work_ steps (of
 // 2^step_log2 keys; sums[r]: those before sequence r).  buf, stats: LDS for the join of a
 // workgroup's waves, not read by others while this runs.
@@ -407,71 +471,18 @@ __device__ __forceinline__ void attend_shares(const AttentionArgs& a, const Line
         }
       }
     }
-    if (!whole) {
-      // Parts join in a tree, kJoin at a time: of the workgroups of a node the last to arrive
-      // adds their parts, in order, and goes on to the next level with the sum.
-      const int parts = share_owner(work, workers, p.at + p.steps - 1) - first + 1;
-      float2* row_sums = KW > 1 ? reinterpret_cast<float2*>(lds) : stats;   // of the node
-      int k0 = b - first;
-      for (int level = 0, stride = 1; stride < parts; ++level, stride *= kJoin) {
-        k0 -= k0 % (stride * kJoin);
-        const int n = min(kJoin, (parts - k0 + stride - 1) / stride);
-        const bool root = stride * kJoin >= parts;
-        if (n == 1) continue;
-        stores_done();
-        lds_barrier();
-        if (tid == 0) {
-          int* arrived = line.arrived() + level * a.counters + first + k0;
-          last_s = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
-          if (last_s) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (!whole)
+      join_tree<DB, kThreads, kRows>(a, line, p, D, tid, b, first, work, workers, KW > 1 ? reinterpret_cast<float2*>(lds) : stats, last_s,
+                                     [&](int lrow, int d, float mm, float ll, f32x4_t acc) {
+        const auto y = out_row(p, lrow);
+        if (keep) {
+          write4(line.state_o() + y.lse * D + d, acc);
+          if (d == 0) state_ml[y.lse] = make_float2(mm, ll);
+          return;
         }
-        lds_barrier();
-        if (!last_s) break;
-        for (int it = tid; it < p.rows * (DB / 4); it += kThreads) {
-          const int lrow = it / (DB / 4), d = it % (DB / 4) * 4;
-          if (d >= D) continue;
-          f32x4_t v[kJoin];
-          float2 x[kJoin];
-#pragma unroll
-          for (int k = 0; k < kJoin; ++k) {
-            const uint32_t at = part_row(k0 + k * stride, lrow);
-            x[k] = get_shared2(part_ml, k < n ? at * 8 : kNowhere);
-            v[k] = get_shared(part_o, k < n ? (at * D + d) * 4 : kNowhere);
-          }
-          float mm = -INFINITY, ll = 0.f;
-          f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < kJoin; ++k)
-            if (k < n) mm = fmaxf(mm, x[k].x);
-#pragma unroll
-          for (int k = 0; k < kJoin; ++k)
-            if (k < n) {
-              const float f = __builtin_amdgcn_exp2f(x[k].x - finite_top(mm));
-              ll += x[k].y * f;
-              acc += v[k] * f;
-            }
-          if (root) {
-            const auto y = out_row(p, lrow);
-            if (keep) {
-              write4(line.state_o() + y.lse * D + d, acc);
-              if (d == 0) state_ml[y.lse] = make_float2(mm, ll);
-              continue;
-            }
-            write4(y.out + d, acc * (ll == 0.f ? 0.f : over_sum(a.c.v_scale, ll)));
-            if (a.lse && d == 0) a.lse[y.lse] = log_sum(mm, ll);
-          } else {
-            const uint32_t at = part_row(k0, lrow);
-            put_shared(part_o, (at * D + d) * 4, acc);
-            // the row's other threads still read its sums: they are written after the loop
-            if (d == 0) row_sums[lrow] = make_float2(mm, ll);
-          }
-        }
-        lds_barrier();
-        if (!root)
-          for (int lrow = tid; lrow < p.rows; lrow += kThreads)
-            put_shared2(part_ml, part_row(k0, lrow) * 8, row_sums[lrow].x, row_sums[lrow].y);
-      }
-    }
+        write4(y.out + d, acc * (ll == 0.f ? 0.f : over_sum(a.c.v_scale, ll)));
+        if (a.lse && d == 0) a.lse[y.lse] = log_sum(mm, ll);
+      });
     lds_barrier();
   };
 

@@ -40,6 +40,7 @@ rax::LineShape line_shape(const rax::AttentionArgs& a, int row_tiles, int row_wa
   s.row_waves = row_waves;
   int least = a.dtype == LORA_F32 ? 4 : 5;
   for (int w = 4 / row_waves; w > 1; w /= 2) ++least;
+  if (row_waves == 4) least = 6;   // wide blocks: tiles of 64 keys
   s.min_steps = std::max(1, std::max(128, 4 << rows_log2) >> least);
   s.step_log2 = rax::line_step_log2(least, units, a.num_tokens, a.max_pages << a.c.page_shift, a.c.heads, a.group_size, rows_log2);
   return s;
@@ -79,10 +80,10 @@ lora_status lora_shared_create(lora_shared** out, int device, int max_seqs, int 
   a->q_heads = num_q_heads;
   a->kv_heads = num_kv_heads;
   a->dim = head_dim;
-  const size_t part = 2 * (size_t)a->workers * rax::kMaxRows * sizeof(float);   // two slots a workgroup
   const size_t state = (size_t)max_tokens * num_q_heads * sizeof(float);
   const size_t counters = sizeof(int) * rax::kJoinLevels * 4 * a->workers;
   for (int i = 0; i < 2 && e == hipSuccess; ++i) {
+    const size_t part = 2 * (size_t)a->workers * (i == 0 ? 128 : rax::kMaxRows) * sizeof(float);   // two slots a workgroup
     e = hipMalloc(reinterpret_cast<void**>(&a->part_o[i]), part * head_dim);
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->part_ml[i]), part * 2);
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->state_o[i]), state * head_dim);
@@ -177,7 +178,9 @@ lora_status lora_shared_attention(const lora_shared* attention, const void* q, i
   const long long group_rows = ((long long)num_tokens + std::max(1, num_groups) - 1) / std::max(1, num_groups) * a.group_size;
   const bool many = seq_rows > 16;
   s.own_line = many ? line_shape(a, 2, 2, num_seqs, 6) : line_shape(a, 1, 1, num_seqs, 4);
-  s.common_line = many || group_rows > 32 ? line_shape(a, 2, 2, num_groups, 6) : line_shape(a, 2, 1, num_groups, 5);
+  const bool wide = group_rows > 64 && dtype == LORA_BF16 && (attention->dim == 64 || attention->dim == 128);
+  s.common_line = wide ? line_shape(a, 1, 4, num_groups, 7)
+                       : many || group_rows > 32 ? line_shape(a, 2, 2, num_groups, 6) : line_shape(a, 2, 1, num_groups, 5);
   if (s.own_line.step_log2 < 0 || s.common_line.step_log2 < 0)
     return fail(LORA_ERR_SHAPE, "num_tokens %d times %d query heads is too much for one call", num_tokens, attention->q_heads);
   // own keys that one block of rows reads, in whole 128-byte lines, need no place in the caches

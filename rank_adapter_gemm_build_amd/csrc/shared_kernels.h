@@ -12,6 +12,7 @@
 
 #include "attention_kernels.h"
 #include "shared.h"
+#include "wide_kernels.h"
 
 namespace rax {
 
@@ -71,13 +72,16 @@ __device__ __forceinline__ LineSums line_sums(int scan, int mine, const int* wav
   return x;
 }
 
-// SRT, SRW: row tiles and row waves of the own line; PRT, PRW: of the common line; ONCE: the own line's cells
+// SRT, SRW: row tiles and row waves of the own line; PRT, PRW: of the common line, PRW = 4: wide blocks; ONCE: the own line's cells
 // pass the caches as a stream
+template <typename C, int DB, int RT, int RW> constexpr int line_lds() {   // 16-byte units
+  if constexpr (RW == 4) return wide_lds<DB>() / 16;
+  else return join_lds<C, DB, RT, 4, RW>();
+}
 template <typename C, int DB, int SRT, int SRW, int PRT, int PRW, bool ONCE>
 __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel(SharedArgs s) {
-  constexpr int kThreads = 256, kOwnRows = 4 + SRT / 2 + SRW / 2, kCommonRows = 4 + PRT / 2 + PRW / 2;
-  constexpr int kJoinUnits = join_lds<C, DB, SRT, 4, SRW>() > join_lds<C, DB, PRT, 4, PRW>() ? join_lds<C, DB, SRT, 4, SRW>()
-                                                                                            : join_lds<C, DB, PRT, 4, PRW>();
+  constexpr int kThreads = 256, kOwnRows = 4 + SRT / 2 + SRW / 2, kCommonRows = PRW == 4 ? kWideRowsLog2 : 4 + PRT / 2 + PRW / 2;
+  constexpr int kOwnLds = line_lds<C, DB, SRT, SRW>(), kCommonLds = line_lds<C, DB, PRT, PRW>(), kJoinUnits = kOwnLds > kCommonLds ? kOwnLds : kCommonLds;
   extern __shared__ float4 lds[];
   __shared__ int part_s[4][2];
   const AttentionArgs& a = s.a;
@@ -144,19 +148,31 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
     if ((turn == 0) == own_first) {
       if (bo < split.own) attend_shares<C, DB, SRT, 4, SRW, ONCE>(a, own_line, lds, own_sums, bo, o.work, split.own, s.own_line.step_log2);
     } else {
-      if (bc < split.common) attend_shares<C, DB, PRT, 4, PRW, false>(a, common_line, lds, common_sums, bc, c.work, split.common, s.common_line.step_log2);
+      if constexpr (PRW == 4) {
+        if (bc < split.common) attend_wide<C, DB>(a, common_line, lds, common_sums, bc, c.work, split.common, s.common_line.step_log2);
+      } else {
+        if (bc < split.common) attend_shares<C, DB, PRT, 4, PRW, false>(a, common_line, lds, common_sums, bc, c.work, split.common, s.common_line.step_log2);
+      }
     }
   }
 }
 
 template <typename C, int DB, int SRT, int SRW, int PRT, int PRW, bool ONCE>
 static void launch_shared_shape(const SharedArgs& s, hipStream_t stream, const KTimer& tm) {
-  constexpr int own = join_lds<C, DB, SRT, 4, SRW>(), common = join_lds<C, DB, PRT, 4, PRW>();
+  constexpr int own = line_lds<C, DB, SRT, SRW>(), common = line_lds<C, DB, PRT, PRW>();
   RAX_LAUNCH(tm, (shared_attention_kernel<C, DB, SRT, SRW, PRT, PRW, ONCE>), dim3(s.a.workers), dim3(256),
              (uint32_t)(16 * (own > common ? own : common) + sizeof(int) * (2 * s.a.num_seqs + 4 * s.num_groups + 1)), stream, s);
 }
 template <typename C, int DB> static void launch_shared_lines(const SharedArgs& s, hipStream_t stream, const KTimer& tm) {
   const bool once = s.a.read_once != 0;
+  if constexpr (sizeof(C) < 4 && DB <= 128) {
+    if (s.common_line.row_waves == 4) {
+      if (s.own_line.row_tiles == 2) launch_shared_shape<C, DB, 2, 2, 1, 4, false>(s, stream, tm);
+      else if (once) launch_shared_shape<C, DB, 1, 1, 1, 4, true>(s, stream, tm);
+      else launch_shared_shape<C, DB, 1, 1, 1, 4, false>(s, stream, tm);
+      return;
+    }
+  }
   if (s.own_line.row_tiles == 2) launch_shared_shape<C, DB, 2, 2, 2, 2, false>(s, stream, tm);
   else if (s.common_line.row_waves == 2 && once) launch_shared_shape<C, DB, 1, 1, 2, 2, true>(s, stream, tm);
   else if (s.common_line.row_waves == 2) launch_shared_shape<C, DB, 1, 1, 2, 2, false>(s, stream, tm);
