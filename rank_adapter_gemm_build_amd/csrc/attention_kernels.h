@@ -239,9 +239,10 @@ struct Part {
 };
 
 // The line of paged attention: what the shares below take from it.  A line with kState keeps the results (m, l, o)
-// of some of its sequences as they are, for a later join with others.
+// of some of its sequences as they are, for a later join with others; one without kTree leaves the parts of units that are
+// shared in the workspace, for a later launch.
 struct PagedLine {
-  static constexpr bool kState = false;
+  static constexpr bool kState = false, kTree = true;
   const AttentionArgs& a;
   __device__ __forceinline__ int count() const { return a.num_seqs; }
   __device__ __forceinline__ SeqRows rows(int r, int max_len) const {
@@ -324,8 +325,8 @@ __device__ __forceinline__ void join_tree(const AttentionArgs& a, const Line& li
 }
 
 // The shares of a line that this workgroup has: share b_ of workers_ equal ones of the line's work_ steps (of
-// 2^step_log2 keys; sums[r]: those before sequence r).  buf, stats: LDS for the join of a
-// workgroup's waves, not read by others while this runs.
+// 2^step_log2 keys; sums[r]: those before sequence r).  lds: for the join of a workgroup's waves, not used by
+// others while this runs; with one wave and no tree none, nor barriers: the waves of a larger workgroup may each have a share.
 // RT: row tiles of a wave; W: waves; RW: those that have rows side by side; ONCE: every line of
 // the cache is read by one workgroup only, and passes the caches as a stream
 template <typename C, int DB, int RT, int W, int RW, bool ONCE, class Line>
@@ -340,7 +341,7 @@ __device__ __forceinline__ void attend_shares(const AttentionArgs& a, const Line
   constexpr int kAux = ONCE ? kStreaming : 0;
   constexpr int kThreads = 64 * W, KW = W / RW;   // KW: waves that split the keys
   constexpr int kRowsLog2 = 4 + RT / 2 + RW / 2, kRows = 1 << kRowsLog2, kKeysLog2 = S::kF32 ? 4 : 5;
-  const int tid = threadIdx.x, lane = lane_id(), w = W == 1 ? 0 : uniform(tid >> 6), rw = w % RW, kw = w / RW;
+  const int lane = lane_id(), tid = W == 1 && !Line::kTree ? lane : (int)threadIdx.x, w = W == 1 ? 0 : uniform(tid >> 6), rw = w % RW, kw = w / RW;
   JoinRows* buf = reinterpret_cast<JoinRows*>(lds);                                  // [W]
   float2* stats = reinterpret_cast<float2*>(buf + (KW > 1 ? W : 0));                 // [W][RT][16]: maxima and sums
   const int c16 = lane & 15, g4 = lane >> 4, group = a.group_size, tiles_log2 = step_log2 - kKeysLog2;   // tiles of a step
@@ -379,7 +380,7 @@ __device__ __forceinline__ void attend_shares(const AttentionArgs& a, const Line
   };
   auto join = [&](const Part& p) {
     const int D = here(a.c.dim), b = here(b_), work = here(work_), workers = here(workers_);
-    const int tid = here_lane((int)threadIdx.x), c16 = tid & 15, g4 = (tid >> 4) & 3;
+    const int tid = here_lane(W == 1 && !Line::kTree ? lane : (int)threadIdx.x), c16 = tid & 15, g4 = (tid >> 4) & 3;
     const bool whole = p.s0 == 0 && p.s1 == p.steps, keep = Line::kState && p.state;
     float2* const state_ml = reinterpret_cast<float2*>(line.state_ml());
     const int first = whole ? b : share_owner(work, workers, p.at);
@@ -471,19 +472,16 @@ __device__ __forceinline__ void attend_shares(const AttentionArgs& a, const Line
         }
       }
     }
-    if (!whole)
-      join_tree<DB, kThreads, kRows>(a, line, p, D, tid, b, first, work, workers, KW > 1 ? reinterpret_cast<float2*>(lds) : stats, last_s,
-                                     [&](int lrow, int d, float mm, float ll, f32x4_t acc) {
-        const auto y = out_row(p, lrow);
-        if (keep) {
-          write4(line.state_o() + y.lse * D + d, acc);
-          if (d == 0) state_ml[y.lse] = make_float2(mm, ll);
-          return;
-        }
-        write4(y.out + d, acc * (ll == 0.f ? 0.f : over_sum(a.c.v_scale, ll)));
-        if (a.lse && d == 0) a.lse[y.lse] = log_sum(mm, ll);
-      });
-    lds_barrier();
+    if constexpr (Line::kTree) {
+      if (!whole)
+        join_tree<DB, kThreads, kRows>(a, line, p, D, tid, b, first, work, workers, KW > 1 ? reinterpret_cast<float2*>(lds) : stats, last_s,
+                                       [&](int lrow, int d, float mm, float ll, f32x4_t acc) {
+          const auto y = out_row(p, lrow);
+          write4(y.out + d, acc * (ll == 0.f ? 0.f : over_sum(a.c.v_scale, ll)));
+          if (a.lse && d == 0) a.lse[y.lse] = log_sum(mm, ll);
+        });
+    }
+    if constexpr (KW > 1 || Line::kTree) lds_barrier();
   };
 
   // ---- the parts of the share; a part's first tile is on its way while the one before is

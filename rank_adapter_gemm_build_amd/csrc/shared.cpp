@@ -27,21 +27,25 @@ struct lora_shared {
   int workers = 0;            // workgroups
   // device, of the common line and of the own line
   float *part_o[2] = {}, *part_ml[2] = {}, *state_o[2] = {}, *state_ml[2] = {};
-  int* arrived[2] = {};       // zero between calls
-  int32_t* from = nullptr;
+  rax::LinePlan* plan = nullptr;   // device, and for the two below
+  rax::SeqPlan* seqs = nullptr;
+  rax::GroupPlan* groups = nullptr;
 };
 
 namespace {
 
-// Shape of a line whose sequences (or groups) have so many rows a kv head.
+// Shape of a line with blocks of 2^rows_log2 rows, waves that split the keys of a step or, with one wave a share, none.
 rax::LineShape line_shape(const rax::AttentionArgs& a, int row_tiles, int row_waves, int units, int rows_log2) {
   rax::LineShape s{};
   s.row_tiles = row_tiles;
   s.row_waves = row_waves;
-  int least = a.dtype == LORA_F32 ? 4 : 5;
-  for (int w = 4 / row_waves; w > 1; w /= 2) ++least;
-  if (row_waves == 4) least = 6;   // wide blocks: tiles of 64 keys
-  s.min_steps = std::max(1, std::max(128, 4 << rows_log2) >> least);
+  s.rows_log2 = rows_log2;
+  int least = a.dtype == LORA_F32 ? 4 : 5;   // keys of a tile
+  if (row_waves == 4) least = rax::kWideKeysLog2;
+  else if (row_waves > 0)
+    for (int w = 4 / row_waves; w > 1; w /= 2) ++least;
+  // at least so many keys a workgroup: fewer cost more in the join than they save
+  s.min_steps = row_waves == 0 ? 1 : std::max(1, std::max(128, 4 << rows_log2) >> least);
   s.step_log2 = rax::line_step_log2(least, units, a.num_tokens, a.max_pages << a.c.page_shift, a.c.heads, a.group_size, rows_log2);
   return s;
 }
@@ -81,18 +85,16 @@ lora_status lora_shared_create(lora_shared** out, int device, int max_seqs, int 
   a->kv_heads = num_kv_heads;
   a->dim = head_dim;
   const size_t state = (size_t)max_tokens * num_q_heads * sizeof(float);
-  const size_t counters = sizeof(int) * rax::kJoinLevels * 4 * a->workers;
   for (int i = 0; i < 2 && e == hipSuccess; ++i) {
-    const size_t part = 2 * (size_t)a->workers * (i == 0 ? 128 : rax::kMaxRows) * sizeof(float);   // two slots a workgroup
+    const size_t part = 2 * (size_t)a->workers * (i == 0 ? 1 << rax::kWideRowsLog2 : rax::kMaxRows) * sizeof(float);   // two slots a workgroup
     e = hipMalloc(reinterpret_cast<void**>(&a->part_o[i]), part * head_dim);
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->part_ml[i]), part * 2);
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->state_o[i]), state * head_dim);
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->state_ml[i]), state * 2);
-    if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->arrived[i]), counters);
-    if (e == hipSuccess) e = hipMemset(a->arrived[i], 0, counters);
   }
-  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->from), max_seqs * sizeof(int32_t));
-  if (e == hipSuccess) e = hipDeviceSynchronize();
+  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->plan), sizeof(rax::LinePlan));
+  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->seqs), max_seqs * sizeof(rax::SeqPlan));
+  if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void**>(&a->groups), max_seqs * sizeof(rax::GroupPlan));
   if (e != hipSuccess) {
     (void)lora_shared_destroy(a);
     return hip_fail(e, "shared attention workspace");
@@ -109,9 +111,10 @@ lora_status lora_shared_destroy(lora_shared* attention) {
     if (attention->part_ml[i]) (void)hipFree(attention->part_ml[i]);
     if (attention->state_o[i]) (void)hipFree(attention->state_o[i]);
     if (attention->state_ml[i]) (void)hipFree(attention->state_ml[i]);
-    if (attention->arrived[i]) (void)hipFree(attention->arrived[i]);
   }
-  if (attention->from) (void)hipFree(attention->from);
+  if (attention->plan) (void)hipFree(attention->plan);
+  if (attention->seqs) (void)hipFree(attention->seqs);
+  if (attention->groups) (void)hipFree(attention->groups);
   delete attention;
   return ok();
 }
@@ -168,16 +171,17 @@ lora_status lora_shared_attention(const lora_shared* attention, const void* q, i
   a.group_size = attention->q_heads / attention->kv_heads;
   a.group = rax::fast_div(a.group_size);
   a.workers = attention->workers / (attention->dim > 128 ? 2 : 1);
-  a.counters = 4 * attention->workers;
   s.group_start = group_start;
   s.common = common_lens;
   s.num_groups = group_start ? num_groups : 0;
-  s.from = attention->from;
+  s.plan = attention->plan;
+  s.seqs = attention->seqs;
+  s.groups = attention->groups;
   // rows a kv head of the mean sequence and the mean group
   const long long seq_rows = ((long long)num_tokens + num_seqs - 1) / num_seqs * a.group_size;
   const long long group_rows = ((long long)num_tokens + std::max(1, num_groups) - 1) / std::max(1, num_groups) * a.group_size;
   const bool many = seq_rows > 16;
-  s.own_line = many ? line_shape(a, 2, 2, num_seqs, 6) : line_shape(a, 1, 1, num_seqs, 4);
+  s.own_line = many ? line_shape(a, 2, 2, num_seqs, 6) : line_shape(a, 1, 0, num_seqs, 4);
   const bool wide = group_rows > 64 && dtype == LORA_BF16 && (attention->dim == 64 || attention->dim == 128);
   s.common_line = wide ? line_shape(a, 1, 4, num_groups, 7)
                        : many || group_rows > 32 ? line_shape(a, 2, 2, num_groups, 6) : line_shape(a, 2, 1, num_groups, 5);
@@ -192,7 +196,6 @@ lora_status lora_shared_attention(const lora_shared* attention, const void* q, i
   for (int i = 0; i < 2; ++i) {
     lines[i]->part_o = attention->part_o[i];
     lines[i]->part_ml = attention->part_ml[i];
-    lines[i]->arrived = attention->arrived[i];
     lines[i]->state_o = attention->state_o[i];
     lines[i]->state_ml = attention->state_ml[i];
   }

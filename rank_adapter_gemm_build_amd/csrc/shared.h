@@ -8,19 +8,33 @@
 
 namespace rax {
 
+constexpr int kWideRowsLog2 = 7, kWideKeysLog2 = 6;   // wide blocks: rows of a workgroup, keys of a tile
 // A line of steps (the common tokens' or the sequences' own) in a launch.
 struct LineShape {
-  int row_tiles, row_waves;          // of a workgroup, as AttentionArgs
-  int min_steps, step_log2;
-  float *part_o, *part_ml;           // as AttentionArgs
-  int* arrived;
-  float *state_o, *state_ml;         // [num_tokens * q_heads][dim], [..][2]: what the merge takes
+  int row_tiles, row_waves;          // of a workgroup, as AttentionArgs (own_line: row_waves 0 for one wave a share)
+  int rows_log2;                     // of a block
+  int min_steps, step_log2;          // least steps of a workgroup (or wave); keys of a step
+  float *part_o, *part_ml;           // as AttentionArgs: results of units that several share
+  float *state_o, *state_ml;         // [num_tokens * q_heads][dim], [..][2]: of whole ones
+};
+// What the first launch tells the merge: steps and shares of both lines; where a sequence's and a group's steps begin on
+// their lines, and what the group has.
+struct SeqPlan {
+  int from, at, group, unused;       // first key of its own line: above 0 where it shares the keys before
+};
+struct GroupPlan {
+  int at, len, start, n;             // common keys in use; first token and tokens
+};
+struct LinePlan {
+  int common_work, common_workers, own_work, own_workers;
 };
 struct SharedArgs {
   AttentionArgs a;                   // its members of a line are not used
   const int32_t *group_start, *common;
   int num_groups;
-  int32_t* from;                     // [num_seqs]: first key of each sequence's own line, 0 where nothing is shared
+  LinePlan* plan;
+  SeqPlan* seqs;                     // [num_seqs]
+  GroupPlan* groups;                 // [num_groups]
   LineShape common_line, own_line;
 };
 hipError_t launch_shared_attention(const SharedArgs& s, hipStream_t stream, const KTimer& tm);

@@ -15,30 +15,82 @@ hipError_t launch_shared_attention(const SharedArgs& s, hipStream_t stream, cons
   return launch_shared_of<uint16_t>(s, stream, tm);
 }
 
-// The rows of a sequence that shares: a workgroup takes every gridDim.y-th of its tokens, 4 dims a thread and step.
+// A workgroup takes every gridDim.y-th token of a sequence, and 256 chunks of 4 dims of its heads.
 template <typename T> __global__ __launch_bounds__(256) void shared_merge_kernel(SharedArgs s, FastDiv per_head) {
   const AttentionArgs& a = s.a;
-  const int r = blockIdx.x, D = a.c.dim, chunks = D / 4;
-  if (s.from[r] == 0) return;
-  const SeqRows x = seq_rows(a.query_start[r], a.query_start[r + 1], a.seq_lens[r], a.num_tokens, a.max_pages << a.c.page_shift);
-  const float2 *ml1 = reinterpret_cast<const float2*>(s.common_line.state_ml), *ml2 = reinterpret_cast<const float2*>(s.own_line.state_ml);
-  for (int i = blockIdx.y; i < x.n; i += gridDim.y)
-    for (int e = threadIdx.x; e < a.q_heads * chunks; e += 256) {
-      const int h = fast_quot(e, per_head), d = (e - h * chunks) * 4;
-      const size_t row = (size_t)(x.start + i) * a.q_heads + h;
-      const float2 u = ml1[row], v = ml2[row];
-      const f32x4_t p = *reinterpret_cast<const f32x4_t*>(s.common_line.state_o + row * D + d);
-      const f32x4_t q = *reinterpret_cast<const f32x4_t*>(s.own_line.state_o + row * D + d);
-      const float m = fmaxf(u.x, v.x), f1 = __builtin_amdgcn_exp2f(u.x - finite_top(m)), f2 = __builtin_amdgcn_exp2f(v.x - finite_top(m));
-      const float l = u.y * f1 + v.y * f2;
-      write4(reinterpret_cast<T*>(a.out) + (size_t)(x.start + i) * a.ldo + (size_t)h * D + d,
-             (p * f1 + q * f2) * (l == 0.f ? 0.f : over_sum(a.c.v_scale, l)));
-      if (a.lse && d == 0) a.lse[row] = log_sum(m, l);
+  const LinePlan plan = *s.plan;
+  const SeqPlan q = s.seqs[blockIdx.x];
+  if (plan.own_work == 0) return;
+  const int D = a.c.dim, chunks = D / 4, group = a.group_size, e = (int)(blockIdx.z * 256 + threadIdx.x);
+  const int h = fast_quot(e, per_head), d = (e - h * chunks) * 4, kh = fast_quot(h, a.group), hg = h - kh * group;
+  if (h >= a.q_heads) return;
+  const SeqRows x = seq_rows(a.query_start[blockIdx.x], a.query_start[blockIdx.x + 1], a.seq_lens[blockIdx.x], a.num_tokens,
+                             a.max_pages << a.c.page_shift);
+  const GroupPlan g = s.groups[q.group];
+  float m, l;
+  f32x4_t o;
+  const auto add = [&](const float2* y, const f32x4_t* v, int n) {   // n results, in order
+    float top = m;
+    for (int k = 0; k < n; ++k) top = fmaxf(top, y[k].x);
+    const float keep = __builtin_amdgcn_exp2f(m - finite_top(top));
+    l *= keep;
+    o *= keep;
+    for (int k = 0; k < n; ++k) {
+      const float f = __builtin_amdgcn_exp2f(y[k].x - finite_top(top));
+      l += y[k].y * f;
+      o += v[k] * f;
     }
+    m = top;
+  };
+  // a row of a unit whose first step is `at`: its state, or its parts, kJoin at a time
+  const auto add_unit = [&](const LineShape& line, int at, int steps, int work, int workers, int lrow, size_t row) {
+    const int first = share_owner(work, workers, at), parts = share_owner(work, workers, at + steps - 1) - first + 1;
+    if (parts == 1) {
+      const float2 y = reinterpret_cast<const float2*>(line.state_ml)[row];
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(line.state_o + row * D + d);
+      add(&y, &v, 1);
+      return;
+    }
+    const auto part_o = cells_at(reinterpret_cast<const char*>(line.part_o), true);   // below 2^31 bytes
+    const auto part_ml = cells_at(reinterpret_cast<const char*>(line.part_ml), true);
+    for (int k0 = 0; k0 < parts; k0 += kJoin) {
+      float2 y[kJoin];
+      f32x4_t v[kJoin];
+#pragma unroll
+      for (int k = 0; k < kJoin; ++k) {
+        const uint32_t p = ((uint32_t)part_slot(first, k0 + k) << line.rows_log2) + (uint32_t)lrow;
+        y[k] = __builtin_bit_cast(float2, load_words<2, 0>(part_ml, k0 + k < parts ? p * 8 : kNowhere, 0));
+        v[k] = __builtin_bit_cast(f32x4_t, load_words<4, 0>(part_o, k0 + k < parts ? (p * D + d) * 4 : kNowhere, 0));
+        if (k0 + k >= parts) y[k].x = -INFINITY;
+      }
+      add(y, v, kJoin);
+    }
+  };
+  const int own_steps = own_span(x, q.from, s.own_line.step_log2).steps, own_blocks = row_blocks(x.n, group, s.own_line.rows_log2);
+  const int common_steps = (int)(((unsigned)g.len + ((1u << s.common_line.step_log2) - 1u)) >> s.common_line.step_log2);
+  const int common_blocks = row_blocks(g.n, group, s.common_line.rows_log2);
+  for (int i = blockIdx.y; i < x.n; i += gridDim.y) {
+    const size_t row = (size_t)(x.start + i) * a.q_heads + h;
+    m = -INFINITY;
+    l = 0.f;
+    o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const int own_row = i * group + hg, own_at = q.at + (kh * own_blocks + (own_row >> s.own_line.rows_log2)) * own_steps;
+    if (q.from == 0 && share_owner(plan.own_work, plan.own_workers, own_at) == share_owner(plan.own_work, plan.own_workers, own_at + own_steps - 1))
+      continue;   // written by the first launch
+    const int r = (x.start + i - g.start) * group + hg;   // of the group's rows, unless sequences overlap
+    if (q.from > 0 && r >= 0 && r < g.n * group) {
+      add_unit(s.common_line, g.at + (kh * common_blocks + (r >> s.common_line.rows_log2)) * common_steps, common_steps, plan.common_work,
+               plan.common_workers, r & ((1 << s.common_line.rows_log2) - 1), row);
+    }
+    add_unit(s.own_line, own_at, own_steps, plan.own_work, plan.own_workers, own_row & ((1 << s.own_line.rows_log2) - 1), row);
+    write4(reinterpret_cast<T*>(a.out) + (size_t)(x.start + i) * a.ldo + (size_t)h * D + d, o * (l == 0.f ? 0.f : over_sum(a.c.v_scale, l)));
+    if (a.lse && d == 0) a.lse[row] = log_sum(m, l);
+  }
 }
 
 hipError_t launch_shared_merge(const SharedArgs& s, hipStream_t stream, const KTimer& tm) {
-  const dim3 grid(s.a.num_seqs, std::min(64, std::max(1, (s.a.num_tokens + s.a.num_seqs - 1) / s.a.num_seqs)));
+  const int tokens = (s.a.num_tokens + s.a.num_seqs - 1) / s.a.num_seqs;
+  const dim3 grid(s.a.num_seqs, std::min(64, std::max(1, tokens)), (s.a.q_heads * s.a.c.dim / 4 + 255) / 256);
   const FastDiv per_head = fast_div(s.a.c.dim / 4);
   if (s.a.dtype == LORA_F32) RAX_LAUNCH(tm, shared_merge_kernel<float>, grid, dim3(256), 0u, stream, s, per_head);
   else RAX_LAUNCH(tm, shared_merge_kernel<uint16_t>, grid, dim3(256), 0u, stream, s, per_head);

@@ -47,7 +47,7 @@ RAX_HD SeqSpan common_span(const SeqRows& s, int step_log2) {
 
 // Workgroups of the two lines in a launch of `grid` (a multiple of the dies), and the first of the own line's.  Where both
 // fit side by side each has its own workgroups; where one needs less than half of the grid it gets what it needs
-// and the other the rest; else every workgroup has a share of both.
+// and the other the rest; else every workgroup has a share of both.  common_min, own_min: least steps of a workgroup.
 struct LineSplit {
   int common, own, own_at;
 };

@@ -5,9 +5,12 @@
 //
 // Two lines of steps as in the paged attention, in one launch: one of the groups, whose "sequence" has the rows of all
 // its members and the common keys, all of which every row sees; one of the sequences with the keys from there on.
-// A launch after it joins the two results of each row.  A sequence that shares nothing writes its
+// A launch after it joins what the rows have in the workspace: parts of units that several shares had, and the results of
+// the two lines.  (The parts are large, and a tree in the first launch, as the paged attention has it, would add them in
+// few workgroups: 64 rows a head over 8000 common tokens 77 us, of them 45 in the tree.)  A whole unit of a sequence that shares nothing writes its
 // output at once.  Where both lines are long each workgroup has a share of both, half of them in the other
-// order, so that on a compute unit the products of one go with the loads of the other.
+// order, so that on a compute unit the products of one go with the loads of the other.  Own keys are often few: each wave
+// takes shares of the own line by itself, with no join in the workgroup.
 #pragma once
 
 #include "attention_kernels.h"
@@ -17,7 +20,7 @@
 namespace rax {
 
 struct OwnLine {
-  static constexpr bool kState = true;
+  static constexpr bool kState = true, kTree = false;
   const SharedArgs& s;
   const int* from_s;
   __device__ __forceinline__ int from(int r) const { return uniform(from_s[r]); }
@@ -34,11 +37,10 @@ struct OwnLine {
   __device__ __forceinline__ float* state_ml() const { return s.own_line.state_ml; }
   __device__ __forceinline__ float* part_o() const { return s.own_line.part_o; }
   __device__ __forceinline__ float* part_ml() const { return s.own_line.part_ml; }
-  __device__ __forceinline__ int* arrived() const { return s.own_line.arrived; }
 };
 
 struct CommonLine {
-  static constexpr bool kState = true;
+  static constexpr bool kState = true, kTree = false;
   const SharedArgs& s;
   const int *group_s, *common_s, *lead_s;   // first sequence, common tokens, first member that takes part
   __device__ __forceinline__ int count() const { return s.num_groups; }
@@ -54,7 +56,6 @@ struct CommonLine {
   __device__ __forceinline__ float* state_ml() const { return s.common_line.state_ml; }
   __device__ __forceinline__ float* part_o() const { return s.common_line.part_o; }
   __device__ __forceinline__ float* part_ml() const { return s.common_line.part_ml; }
-  __device__ __forceinline__ int* arrived() const { return s.common_line.arrived; }
 };
 
 // Steps before this thread's run of `mine`, and the whole line's, from the scans of all waves
@@ -72,15 +73,16 @@ __device__ __forceinline__ LineSums line_sums(int scan, int mine, const int* wav
   return x;
 }
 
-// SRT, SRW: row tiles and row waves of the own line; PRT, PRW: of the common line, PRW = 4: wide blocks; ONCE: the own line's cells
-// pass the caches as a stream
+// SRT, SRW: row tiles and row waves of the own line, SRW = 0: one wave a share; PRT, PRW: of the common line, PRW = 4: wide
+// blocks; ONCE: the own line's cells pass the caches as a stream
 template <typename C, int DB, int RT, int RW> constexpr int line_lds() {   // 16-byte units
   if constexpr (RW == 4) return wide_lds<DB>() / 16;
+  else if constexpr (RW == 0) return 0;
   else return join_lds<C, DB, RT, 4, RW>();
 }
 template <typename C, int DB, int SRT, int SRW, int PRT, int PRW, bool ONCE>
 __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel(SharedArgs s) {
-  constexpr int kThreads = 256, kOwnRows = 4 + SRT / 2 + SRW / 2, kCommonRows = PRW == 4 ? kWideRowsLog2 : 4 + PRT / 2 + PRW / 2;
+  constexpr int kThreads = 256, kOwnRows = SRW == 0 ? 4 : 4 + SRT / 2 + SRW / 2, kCommonRows = PRW == 4 ? kWideRowsLog2 : 4 + PRT / 2 + PRW / 2;
   constexpr int kOwnLds = line_lds<C, DB, SRT, SRW>(), kCommonLds = line_lds<C, DB, PRT, PRW>(), kJoinUnits = kOwnLds > kCommonLds ? kOwnLds : kCommonLds;
   extern __shared__ float4 lds[];
   __shared__ int part_s[4][2];
@@ -91,9 +93,13 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
       *lead_s = common_sums + groups, *common_s = lead_s + groups, *group_s = common_s + groups;   // group_s: one longer
 
   // ---- groups, then the sequences' own line, then the common one
+  constexpr int kOwnWaves = SRW == 0 ? 4 : 1;   // shares of the own line that a workgroup has
   for (int g = tid; groups > 0 && g <= groups; g += kThreads) {
     group_s[g] = clamp_int(s.group_start[g], 0, n);
-    if (g < groups) common_s[g] = clamp_int(s.common[g], 0, max_len);
+    if (g < groups) {
+      common_s[g] = clamp_int(s.common[g], 0, max_len);
+      lead_s[g] = n;
+    }
   }
   lds_barrier();
   const int per = (n + kThreads - 1) / kThreads, r0 = min(n, tid * per), r1 = min(n, r0 + per);
@@ -103,6 +109,7 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
     const int g = group_of(group_s, groups, i), from = g >= 0 ? own_from(x, common_s[g], max_len) : 0;
     const long long all = (long long)(a.c.heads * row_blocks(x.n, group, kOwnRows)) * own_span(x, from, s.own_line.step_log2).steps;
     from_s[i] = from;
+    if (from > 0) (void)__hip_atomic_fetch_min(lead_s + g, i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     own_sums[i] = own;
     own = sat_add(own, all < kPlanCap ? (int)all : kPlanCap);
   }
@@ -110,12 +117,8 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
   const int gper = (groups + kThreads - 1) / kThreads, g0 = min(groups, tid * gper), g1 = min(groups, g0 + gper);
   int common = 0;
   for (int g = g0; g < g1; ++g) {
-    const int first = group_s[g], end = group_s[g + 1];
-    int lead = first;
-    while (lead < end && from_s[lead] == 0) ++lead;
-    if (lead >= end) common_s[g] = 0;   // no sequence takes part (read by others before the last barrier only)
-    lead_s[g] = lead < n ? lead : 0;
-    const SeqRows x = seq_rows(a.query_start[first], a.query_start[end], lead < end ? common_s[g] : 0, a.num_tokens, max_len);
+    if (lead_s[g] >= n) lead_s[g] = common_s[g] = 0;   // no sequence takes part (read by others before the last barrier only)
+    const SeqRows x = seq_rows(a.query_start[group_s[g]], a.query_start[group_s[g + 1]], common_s[g], a.num_tokens, max_len);
     const long long all = (long long)(a.c.heads * row_blocks(x.n, group, kCommonRows)) * common_span(x, s.common_line.step_log2).steps;
     common_sums[g] = common;
     common = sat_add(common, all < kPlanCap ? (int)all : kPlanCap);
@@ -129,13 +132,20 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
   const LineSums o = line_sums(own_scan, own, &part_s[0][0], 2, w), c = line_sums(common_scan, common, &part_s[0][1], 2, w);
   // no work, or more than the host counted with: sequences that overlap (the sums are capped)
   const bool fits = o.work < kPlanCap && c.work < kPlanCap;
-  if (blockIdx.x == 0)
-    for (int i = r0; i < r1; ++i) s.from[i] = fits ? from_s[i] : 0;
-  if (!fits || o.work == 0) return;
+  const int grid = (int)gridDim.x, block = (int)blockIdx.x;
+  const LineSplit split = split_lines(c.work, s.common_line.min_steps, o.work, kOwnWaves * s.own_line.min_steps, grid);
+  const int own_workers = min(kOwnWaves * split.own, (o.work + s.own_line.min_steps - 1) / s.own_line.min_steps);
   for (int i = r0; i < r1; ++i) own_sums[i] += o.before;
   for (int g = g0; g < g1; ++g) common_sums[g] += c.before;
-  const int grid = (int)gridDim.x, block = (int)blockIdx.x;
-  const LineSplit split = split_lines(c.work, s.common_line.min_steps, o.work, s.own_line.min_steps, grid);
+  if (block == 0) {   // for the merge
+    if (tid == 0) *s.plan = fits ? LinePlan{c.work, split.common, o.work, own_workers} : LinePlan{0, 0, 0, 0};
+    for (int i = r0; i < r1; ++i) s.seqs[i] = SeqPlan{from_s[i], own_sums[i], from_s[i] > 0 ? group_of(group_s, groups, i) : 0, 0};
+    for (int g = g0; g < g1; ++g) {
+      const SeqRows x = seq_rows(a.query_start[group_s[g]], a.query_start[group_s[g + 1]], common_s[g], a.num_tokens, max_len);
+      s.groups[g] = GroupPlan{common_sums[g], x.len, x.start, x.n};
+    }
+  }
+  if (!fits || o.work == 0) return;
   const int bc = split.common > 0 ? share_of_block(block, split.common) : split.common;
   const int bo = block >= split.own_at ? share_of_block(block - split.own_at, split.own) : split.own;
   if (bc >= split.common && bo >= split.own) return;
@@ -146,7 +156,13 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
 #pragma unroll 1
   for (int turn = 0; turn < 2; ++turn) {
     if ((turn == 0) == own_first) {
-      if (bo < split.own) attend_shares<C, DB, SRT, 4, SRW, ONCE>(a, own_line, lds, own_sums, bo, o.work, split.own, s.own_line.step_log2);
+      if constexpr (SRW == 0) {
+        if (bo < split.own && 4 * bo + w < own_workers)
+          attend_shares<C, DB, SRT, 1, 1, ONCE>(a, own_line, lds, own_sums, 4 * bo + w, o.work, own_workers, s.own_line.step_log2);
+        lds_barrier();   // the waves are together again
+      } else {
+        if (bo < split.own) attend_shares<C, DB, SRT, 4, SRW, ONCE>(a, own_line, lds, own_sums, bo, o.work, split.own, s.own_line.step_log2);
+      }
     } else {
       if constexpr (PRW == 4) {
         if (bc < split.common) attend_wide<C, DB>(a, common_line, lds, common_sums, bc, c.work, split.common, s.common_line.step_log2);
@@ -168,16 +184,16 @@ template <typename C, int DB> static void launch_shared_lines(const SharedArgs& 
   if constexpr (sizeof(C) < 4 && DB <= 128) {
     if (s.common_line.row_waves == 4) {
       if (s.own_line.row_tiles == 2) launch_shared_shape<C, DB, 2, 2, 1, 4, false>(s, stream, tm);
-      else if (once) launch_shared_shape<C, DB, 1, 1, 1, 4, true>(s, stream, tm);
-      else launch_shared_shape<C, DB, 1, 1, 1, 4, false>(s, stream, tm);
+      else if (once) launch_shared_shape<C, DB, 1, 0, 1, 4, true>(s, stream, tm);
+      else launch_shared_shape<C, DB, 1, 0, 1, 4, false>(s, stream, tm);
       return;
     }
   }
   if (s.own_line.row_tiles == 2) launch_shared_shape<C, DB, 2, 2, 2, 2, false>(s, stream, tm);
-  else if (s.common_line.row_waves == 2 && once) launch_shared_shape<C, DB, 1, 1, 2, 2, true>(s, stream, tm);
-  else if (s.common_line.row_waves == 2) launch_shared_shape<C, DB, 1, 1, 2, 2, false>(s, stream, tm);
-  else if (once) launch_shared_shape<C, DB, 1, 1, 2, 1, true>(s, stream, tm);
-  else launch_shared_shape<C, DB, 1, 1, 2, 1, false>(s, stream, tm);
+  else if (s.common_line.row_waves == 2 && once) launch_shared_shape<C, DB, 1, 0, 2, 2, true>(s, stream, tm);
+  else if (s.common_line.row_waves == 2) launch_shared_shape<C, DB, 1, 0, 2, 2, false>(s, stream, tm);
+  else if (once) launch_shared_shape<C, DB, 1, 0, 2, 1, true>(s, stream, tm);
+  else launch_shared_shape<C, DB, 1, 0, 2, 1, false>(s, stream, tm);
 }
 template <typename C> hipError_t launch_shared_of(const SharedArgs& s, hipStream_t stream, const KTimer& tm) {
   if (s.a.c.dim <= 64) launch_shared_lines<C, 64>(s, stream, tm);

@@ -16,13 +16,14 @@
 #pragma once
 
 #include "attention_kernels.h"
+#include "shared.h"
 
 namespace rax {
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kWideRowsLog2 = 7, kWideRows = 1 << kWideRowsLog2, kWideKeysLog2 = 6, kWideKeys = 1 << kWideKeysLog2;
+constexpr int kWideRows = 1 << kWideRowsLog2, kWideKeys = 1 << kWideKeysLog2;
 constexpr float kSlack = 6.f;
 constexpr int kSchedProducts = 0x8, kSchedReads = 0x100;   // instruction classes of a schedule: matrix products, LDS reads
 // bytes of LDS: two tiles of keys and values
@@ -56,8 +57,6 @@ __device__ __forceinline__ void attend_wide(const AttentionArgs& a, const Line l
   constexpr int kPieces = kTile / 1024 / 4;        // 1 KiB pieces of a tile that a wave moves
   constexpr int kPieceKeys = 1024 / (D * 2);       // keys of a piece
   constexpr int KS = D / 16, MB = D / 32;          // contraction steps of the first product, blocks of dims of the second
-  __shared__ int last_s;
-  __shared__ float2 row_sums[kWideRows];
   const int tid = threadIdx.x, lane = lane_id(), w = uniform(tid >> 6), r32 = lane & 31, h = lane >> 5;
   const int ps = a.c.page_shift, max_len = a.max_pages << ps, group = a.group_size;
   const bool flip = a.scale < 0.f;                 // the products of -q: the scale is then positive
@@ -311,7 +310,7 @@ __device__ __forceinline__ void attend_wide(const AttentionArgs& a, const Line l
       if (t + 1 < t1) commit(half ^ 1);
     }
 
-    // ---- the part's results: the rows' state, or a place in the workspace and the tree
+    // ---- the part's results: the rows' state, or a place in the workspace
     {
       const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
       l = __uint_as_float(y[0]) + __uint_as_float(y[1]);
@@ -337,13 +336,6 @@ __device__ __forceinline__ void attend_wide(const AttentionArgs& a, const Line l
           else put_shared(part_o, (place * D + d) * 4, y);
         }
     }
-    if (!whole)
-      join_tree<D, 256, kWideRows>(a, line, p, D, tid, b_, first, work_, workers_, row_sums, last_s, [&](int lr, int d, float mm, float ll, f32x4_t acc) {
-        const int row_ = p.row0 + lr, i = fast_quot(row_, a.group), hh = p.kh * group + row_ - i * group;
-        const size_t at = (size_t)(p.start + i) * a.q_heads + hh;
-        write4(line.state_o() + at * D + d, acc);
-        if (d == 0) state_ml[at] = make_float2(mm, ll);
-      });
     lds_barrier();
     x = p.at + p.s1;
   }
