@@ -9,6 +9,7 @@
 namespace rax {
 
 constexpr int kWideRowsLog2 = 7, kWideKeysLog2 = 6;   // wide blocks: rows of a workgroup, keys of a tile
+constexpr int kEvenGroups = 16;    // most groups whose wide units are cut in even parts
 // A line of steps (the common tokens' or the sequences' own) in a launch.
 struct LineShape {
   int row_tiles, row_waves;          // of a workgroup, as AttentionArgs (own_line: row_waves 0 for one wave a share)
@@ -23,7 +24,7 @@ struct SeqPlan {
   int from, at, group, unused;       // first key of its own line: above 0 where it shares the keys before
 };
 struct GroupPlan {
-  int at, len, start, n;             // common keys in use; first token and tokens
+  int at, steps, start, n;           // steps of a unit; first token and tokens
 };
 struct LinePlan {
   int common_work, common_workers, own_work, own_workers;

@@ -67,7 +67,6 @@ template <typename T> __global__ __launch_bounds__(256) void shared_merge_kernel
     }
   };
   const int own_steps = own_span(x, q.from, s.own_line.step_log2).steps, own_blocks = row_blocks(x.n, group, s.own_line.rows_log2);
-  const int common_steps = (int)(((unsigned)g.len + ((1u << s.common_line.step_log2) - 1u)) >> s.common_line.step_log2);
   const int common_blocks = row_blocks(g.n, group, s.common_line.rows_log2);
   for (int i = blockIdx.y; i < x.n; i += gridDim.y) {
     const size_t row = (size_t)(x.start + i) * a.q_heads + h;
@@ -79,7 +78,7 @@ template <typename T> __global__ __launch_bounds__(256) void shared_merge_kernel
       continue;   // written by the first launch
     const int r = (x.start + i - g.start) * group + hg;   // of the group's rows, unless sequences overlap
     if (q.from > 0 && r >= 0 && r < g.n * group) {
-      add_unit(s.common_line, g.at + (kh * common_blocks + (r >> s.common_line.rows_log2)) * common_steps, common_steps, plan.common_work,
+      add_unit(s.common_line, g.at + (kh * common_blocks + (r >> s.common_line.rows_log2)) * g.steps, g.steps, plan.common_work,
                plan.common_workers, r & ((1 << s.common_line.rows_log2) - 1), row);
     }
     add_unit(s.own_line, own_at, own_steps, plan.own_work, plan.own_workers, own_row & ((1 << s.own_line.rows_log2) - 1), row);

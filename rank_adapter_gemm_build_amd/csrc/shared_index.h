@@ -45,6 +45,25 @@ RAX_HD SeqSpan common_span(const SeqRows& s, int step_log2) {
   return x;
 }
 
+// The units of a group cut in even parts of at most `most` steps: their number, and the steps of a part.
+struct EvenParts {
+  int parts, steps;
+};
+RAX_HD EvenParts even_parts(int steps, int most) {
+  EvenParts x{0, 1};
+  if (steps > 0) {
+    x.parts = (int)(((unsigned)steps + (unsigned)most - 1u) / (unsigned)most);
+    x.steps = (int)(((unsigned)steps + (unsigned)x.parts - 1u) / (unsigned)x.parts);
+    x.parts = (int)(((unsigned)steps + (unsigned)x.steps - 1u) / (unsigned)x.steps);   // none is empty
+  }
+  return x;
+}
+// The i-th size tried for them, from the least possible one to an eighth more.
+RAX_HD int even_most(int work, int workers, int i) {
+  const int least = (int)(((unsigned)work + (unsigned)workers - 1u) / (unsigned)workers);
+  return least + (int)(((long long)least * i) >> 9);
+}
+
 // Workgroups of the two lines in a launch of `grid` (a multiple of the dies), and the first of the own line's.  Where both
 // fit side by side each has its own workgroups; where one needs less than half of the grid it gets what it needs
 // and the other the rest; else every workgroup has a share of both.  common_min, own_min: least steps of a workgroup.

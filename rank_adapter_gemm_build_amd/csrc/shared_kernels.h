@@ -43,12 +43,18 @@ struct CommonLine {
   static constexpr bool kState = true, kTree = false;
   const SharedArgs& s;
   const int *group_s, *common_s, *lead_s;   // first sequence, common tokens, first member that takes part
+  const int* even_s;                        // steps that count as one, where units are cut evenly
   __device__ __forceinline__ int count() const { return s.num_groups; }
   __device__ __forceinline__ SeqRows rows(int g, int max_len) const {
     const const_words_t starts = const_words(s.a.query_start);
     return seq_rows(starts[uniform(group_s[g])], starts[uniform(group_s[g + 1])], uniform(common_s[g]), s.a.num_tokens, max_len);
   }
-  __device__ __forceinline__ SeqSpan span(int, const SeqRows& x, int step_log2) const { return common_span(x, step_log2); }
+  __device__ __forceinline__ int merged(int g) const { return even_s ? uniform(even_s[g]) : 1; }
+  __device__ __forceinline__ SeqSpan span(int g, const SeqRows& x, int step_log2) const {
+    SeqSpan y = common_span(x, step_log2);
+    if (even_s) y.steps = (int)(((unsigned)y.steps + (unsigned)merged(g) - 1u) / (unsigned)merged(g));
+    return y;
+  }
   __device__ __forceinline__ KeyRange keys(int, int, const SeqRows& x) const { return KeyRange{0, x.len}; }
   __device__ __forceinline__ int table_row(int g) const { return uniform(lead_s[g]); }
   __device__ __forceinline__ bool state(int) const { return true; }
@@ -86,6 +92,7 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
   constexpr int kOwnLds = line_lds<C, DB, SRT, SRW>(), kCommonLds = line_lds<C, DB, PRT, PRW>(), kJoinUnits = kOwnLds > kCommonLds ? kOwnLds : kCommonLds;
   extern __shared__ float4 lds[];
   __shared__ int part_s[4][2];
+  __shared__ int units_s[kEvenGroups], steps_s[kEvenGroups], even_s[kEvenGroups];   // wide units: of each group, their steps, steps that count as one
   const AttentionArgs& a = s.a;
   const int n = a.num_seqs, groups = s.num_groups, max_len = a.max_pages << a.c.page_shift, group = a.group_size;
   const int tid = threadIdx.x, lane = lane_id(), w = uniform(tid >> 6);
@@ -119,7 +126,12 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
   for (int g = g0; g < g1; ++g) {
     if (lead_s[g] >= n) lead_s[g] = common_s[g] = 0;   // no sequence takes part (read by others before the last barrier only)
     const SeqRows x = seq_rows(a.query_start[group_s[g]], a.query_start[group_s[g + 1]], common_s[g], a.num_tokens, max_len);
-    const long long all = (long long)(a.c.heads * row_blocks(x.n, group, kCommonRows)) * common_span(x, s.common_line.step_log2).steps;
+    const int units = a.c.heads * row_blocks(x.n, group, kCommonRows), steps = common_span(x, s.common_line.step_log2).steps;
+    const long long all = (long long)units * steps;
+    if (PRW == 4 && g < kEvenGroups) {
+      units_s[g] = units;
+      steps_s[g] = steps;
+    }
     common_sums[g] = common;
     common = sat_add(common, all < kPlanCap ? (int)all : kPlanCap);
   }
@@ -129,20 +141,44 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
     part_s[w][1] = common_scan;
   }
   lds_barrier();
-  const LineSums o = line_sums(own_scan, own, &part_s[0][0], 2, w), c = line_sums(common_scan, common, &part_s[0][1], 2, w);
+  const LineSums o = line_sums(own_scan, own, &part_s[0][0], 2, w);
+  LineSums c = line_sums(common_scan, common, &part_s[0][1], 2, w);
   // no work, or more than the host counted with: sequences that overlap (the sums are capped)
   const bool fits = o.work < kPlanCap && c.work < kPlanCap;
   const int grid = (int)gridDim.x, block = (int)blockIdx.x;
-  const LineSplit split = split_lines(c.work, s.common_line.min_steps, o.work, kOwnWaves * s.own_line.min_steps, grid);
+  LineSplit split = split_lines(c.work, s.common_line.min_steps, o.work, kOwnWaves * s.own_line.min_steps, grid);
   const int own_workers = min(kOwnWaves * split.own, (o.work + s.own_line.min_steps - 1) / s.own_line.min_steps);
   for (int i = r0; i < r1; ++i) own_sums[i] += o.before;
+  // Wide units of one head, whose workgroups should read the same keys at the same time, are cut in even parts where that
+  // costs at most an eighth more for the largest share: the least of 64 sizes with which there are workgroups for all parts.
+  bool even = false;
+  if (PRW == 4 && groups <= kEvenGroups && fits && c.work > 0) {
+    const int most = even_most(c.work, split.common, lane);
+    long long shares = 0;
+    for (int g = 0; g < groups; ++g) shares += (long long)units_s[g] * even_parts(steps_s[g], most).parts;
+    const uint64_t good = __builtin_amdgcn_ballot_w64(shares <= split.common);
+    even = good != 0;
+    if (even) {
+      const int size = even_most(c.work, split.common, __builtin_ctzll(good));
+      c = LineSums{0, 0};
+      for (int g = 0; g < groups; ++g) {
+        const EvenParts y = even_parts(steps_s[g], size);
+        if (g < g0) c.before += units_s[g] * y.parts;
+        if (g == tid) even_s[g] = y.steps;
+        if (g >= g0 && g < g1) common_sums[g] = 0;
+        c.work += units_s[g] * y.parts;
+      }
+      c.work = split.common = uniform(c.work);
+    }
+  }
   for (int g = g0; g < g1; ++g) common_sums[g] += c.before;
   if (block == 0) {   // for the merge
     if (tid == 0) *s.plan = fits ? LinePlan{c.work, split.common, o.work, own_workers} : LinePlan{0, 0, 0, 0};
     for (int i = r0; i < r1; ++i) s.seqs[i] = SeqPlan{from_s[i], own_sums[i], from_s[i] > 0 ? group_of(group_s, groups, i) : 0, 0};
     for (int g = g0; g < g1; ++g) {
       const SeqRows x = seq_rows(a.query_start[group_s[g]], a.query_start[group_s[g + 1]], common_s[g], a.num_tokens, max_len);
-      s.groups[g] = GroupPlan{common_sums[g], x.len, x.start, x.n};
+      const int steps = common_span(x, s.common_line.step_log2).steps;
+      s.groups[g] = GroupPlan{common_sums[g], even ? (int)(((unsigned)steps + (unsigned)even_s[g] - 1u) / (unsigned)even_s[g]) : steps, x.start, x.n};
     }
   }
   if (!fits || o.work == 0) return;
@@ -151,7 +187,7 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
   if (bc >= split.common && bo >= split.own) return;
   lds_barrier();
   const OwnLine own_line{s, from_s};
-  const CommonLine common_line{s, group_s, common_s, lead_s};
+  const CommonLine common_line{s, group_s, common_s, lead_s, even ? even_s : nullptr};
   const bool own_first = 2 * block >= grid;
 #pragma unroll 1
   for (int turn = 0; turn < 2; ++turn) {

@@ -182,7 +182,8 @@ __device__ __forceinline__ void attend_wide(const AttentionArgs& a, const Line l
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[mb][i] = 0.f;
-    const unsigned t0 = (unsigned)p.s0, t1 = (unsigned)p.s1;
+    const unsigned per_step = (unsigned)line.merged(r) << (step_log2 - kWideKeysLog2);   // tiles
+    const unsigned t0 = (unsigned)p.s0 * per_step, t1 = min((unsigned)p.s1 * per_step, (keys + kWideKeys - 1u) / kWideKeys);
     int page[4], page_next[4];
     page_ids(t0, page);
     issue(t0, page, 0);
