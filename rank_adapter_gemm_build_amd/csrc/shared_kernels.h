@@ -201,6 +201,9 @@ __global__ __launch_bounds__(256, DB > 128 ? 1 : 2) void shared_attention_kernel
       }
     } else {
       if constexpr (PRW == 4) {
+        // Those that begin later take precedence on their compute unit over those that have been at it since the start: both
+        // end at about the same time (256 sequences with 32000 common tokens 421 -> 402 us).
+        if (own_first) __builtin_amdgcn_s_setprio(1);
         if (bc < split.common) attend_wide<C, DB>(a, common_line, lds, common_sums, bc, c.work, split.common, s.common_line.step_log2);
       } else {
         if (bc < split.common) attend_shares<C, DB, PRT, 4, PRW, false>(a, common_line, lds, common_sums, bc, c.work, split.common, s.common_line.step_log2);
