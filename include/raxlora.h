@@ -660,9 +660,10 @@ lora_status lora_beam_select(const lora_beams* beams, const void* logits, int ld
  * Invalid entries: a parent outside [-1, num_rows) (taken as -1), a length outside [0, max_pages * page_size] (the
  * row holds nothing), a page id outside [0, num_pages) in the used part of a row or among the drawn (-1 in the new
  * row, nothing copied), pages given back beyond the ring's places.  scratch[(num_pages + 31) / 32] and cursor[2..3] are scratch words,
- * zero between calls.  No vector may overlap another.  Rows may name any row as parent, several the same.
+ * zero between calls.  No vector may overlap another (the table from its first
+ * used entry to its last).  Rows may name any row as parent, several the same.
  * One launch on `stream` of `device`; two calls that share a cursor, or a call and a page plan, must not overlap in time.
- * Errors: INVALID_ARG (a NULL pointer), SHAPE (num_rows outside [0, LORA_MAX_SEQS], page_size, num_pages, max_pages,
+ * Errors: INVALID_ARG (a NULL pointer, vectors that overlap), SHAPE (num_rows outside [0, LORA_MAX_SEQS], page_size, num_pages, max_pages,
  * ld_table as lora_page_plan).  num_rows = 0 does nothing.
  */
 lora_status lora_page_fork(int device, const int32_t* parents, int num_rows, int32_t* lens, int page_size, int num_pages,
@@ -684,8 +685,8 @@ lora_status lora_page_copy(int device, const lora_kv_cache* layers, int num_laye
 
 /*
  * Shared attention for up to max_seqs sequences and max_tokens new tokens (owns the workspace: the two results
- * of every row, 8 bytes * max_tokens * num_q_heads * (head_dim + 2), partial results of 1 MiB a head_dim value
- * on 256 compute units, and counters).  Arguments and errors of create as lora_attention_create.
+ * of every row, 8 bytes * max_tokens * num_q_heads * (head_dim + 2), partial results of 768 KiB a head_dim value
+ * on 256 compute units, and 48 bytes * max_seqs).  Arguments and errors of create as lora_attention_create.
  */
 typedef struct lora_shared lora_shared;
 lora_status lora_shared_create(lora_shared** out, int device, int max_seqs, int max_tokens,

@@ -174,10 +174,6 @@ template <typename C, int DB> struct AttnTile {
   static constexpr int kPitch = 16 * kEC + 4;                  // floats of a row in the join buffer
 };
 
-// workspace slot of part p of a unit that begins in workgroup `first`: a workgroup's
-// second slot is the unit's that begins in it, its first the one's that began before
-__device__ __forceinline__ int part_slot(int first, int p) { return p == 0 ? 2 * first + 1 : 2 * (first + p); }
-
 // a word of cells with those that are not finite cleared (e4m3 has no infinities)
 template <typename C> __device__ __forceinline__ uint32_t without_odd(uint32_t v) {
   if constexpr (sizeof(C) == 4) return (v & 0x7f800000u) == 0x7f800000u ? 0u : v;

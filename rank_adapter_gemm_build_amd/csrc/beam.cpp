@@ -39,7 +39,7 @@ namespace {
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
+  return a && b && na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
 }  // namespace
@@ -161,6 +161,16 @@ lora_status lora_page_fork(int device, const int32_t* parents, int num_rows, int
   if (max_pages < 1 || (long long)max_pages * page_size > 0x7fffffffLL)
     return fail(LORA_ERR_SHAPE, "max_pages %d outside [1, (2^31 - 1) / page_size]", max_pages);
   if (ld_table < max_pages) return fail(LORA_ERR_SHAPE, "ld_table = %d < max_pages = %d", ld_table, max_pages);
+  // the workgroups of a call read and write these at the same time
+  const size_t rows = num_rows, pages = num_pages, table = rows > 0 ? (rows - 1) * ld_table + max_pages : 0;
+  const struct {
+    const void* at;
+    size_t words;
+  } vecs[] = {{parents, rows},     {lens, rows},     {copy_src, rows},     {copy_dst, rows},            {copy_tokens, rows}, {free_pages, pages},
+              {cursor, 4}, {shares, pages}, {block_table, table}, {scratch, (pages + 31) / 32}, {meta, LORA_FORK_META}};
+  for (const auto& x : vecs)
+    for (const auto* y = vecs; y != &x; ++y)
+      if (overlap(x.at, 4 * x.words, y->at, 4 * y->words)) return fail(LORA_ERR_INVALID_ARG, "two vectors overlap");
   if (num_rows == 0) return ok();
   DeviceGuard g(device);
   if (g.err != hipSuccess) return hip_fail(g.err, "hipSetDevice");

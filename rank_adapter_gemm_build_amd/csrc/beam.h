@@ -26,7 +26,7 @@ struct BeamArgs {
 };
 constexpr int kBeamWaves = 4, kBeamLoads = 4;                  // waves of a workgroup; 16-byte loads of a lane and tile
 constexpr int kBeamTileBytes = kBeamLoads * 64 * 16;           // of a wave
-constexpr int kBeamMaxWaves = 3072;                             // of a launch whose waves have one tile each
+constexpr int kBeamMaxWaves = 12 * 256;                         // of a launch whose waves have one tile each
 int beam_segs(long long rows, int vocab, int size);            // workgroups that share a row of such values
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t stream, const KTimer& tm);
 

@@ -151,6 +151,10 @@ RAX_HD int share_owner(int work, int g, int x) {
   return (int)((unsigned)x < wide ? (unsigned)x / (q + 1u) : rem + ((unsigned)x - wide) / q);
 }
 
+// Workspace slot of part p of a unit that begins in workgroup `first`: a workgroup's
+// second slot is the unit's that begins in it, its first the one's that began before.
+RAX_HD int part_slot(int first, int p) { return p == 0 ? 2 * first + 1 : 2 * (first + p); }
+
 // Division by a fixed d in [1, 2^16] of numbers below 2^31: with s = floor(log2 d), n / d =
 // (n ceil(2^(32 + s) / d)) >> (32 + s), as the multiplier's excess, below d < 2^(s + 1),
 // times n stays below 2^(32 + s); a power of two is the shift alone (mul 0).

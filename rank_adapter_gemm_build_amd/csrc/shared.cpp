@@ -182,8 +182,9 @@ lora_status lora_shared_attention(const lora_shared* attention, const void* q, i
   const long long group_rows = ((long long)num_tokens + std::max(1, num_groups) - 1) / std::max(1, num_groups) * a.group_size;
   const bool many = seq_rows > 16;
   s.own_line = many ? line_shape(a, 2, 2, num_seqs, 6) : line_shape(a, 1, 0, num_seqs, 4);
-  const bool wide = group_rows > 64 && dtype == LORA_BF16 && (attention->dim == 64 || attention->dim == 128);
-  s.common_line = wide ? line_shape(a, 1, 4, num_groups, 7)
+  // above kWideGroups groups their tables do not fit into LDS beside the tiles
+  const bool wide = group_rows > 64 && dtype == LORA_BF16 && (attention->dim == 64 || attention->dim == 128) && num_groups <= rax::kWideGroups;
+  s.common_line = wide ? line_shape(a, 1, 4, num_groups, rax::kWideRowsLog2)
                        : many || group_rows > 32 ? line_shape(a, 2, 2, num_groups, 6) : line_shape(a, 2, 1, num_groups, 5);
   if (s.own_line.step_log2 < 0 || s.common_line.step_log2 < 0)
     return fail(LORA_ERR_SHAPE, "num_tokens %d times %d query heads is too much for one call", num_tokens, attention->q_heads);

@@ -9,6 +9,7 @@
 namespace rax {
 
 constexpr int kWideRowsLog2 = 7, kWideKeysLog2 = 6;   // wide blocks: rows of a workgroup, keys of a tile
+constexpr int kWideGroups = 1024;  // most groups of a call that has them
 constexpr int kEvenGroups = 16;    // most groups whose wide units are cut in even parts
 // A line of steps (the common tokens' or the sequences' own) in a launch.
 struct LineShape {
