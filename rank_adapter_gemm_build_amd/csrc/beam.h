@@ -27,6 +27,9 @@ struct BeamArgs {
 constexpr int kBeamWaves = 4, kBeamLoads = 4;                  // waves of a workgroup; 16-byte loads of a lane and tile
 constexpr int kBeamTileBytes = kBeamLoads * 64 * 16;           // of a wave
 constexpr int kBeamMaxWaves = 12 * 256;                         // of a launch whose waves have one tile each
+// Most lists of a request, rows times workgroups of a row: with p tiles a wave, rows * tiles < (p + 1) kBeamMaxWaves, there are
+// at most rows * (tiles / (p kBeamWaves) + 1).
+constexpr int kBeamMaxLists = 2 * kBeamMaxWaves / kBeamWaves + LORA_MAX_BEAMS;
 int beam_segs(long long rows, int vocab, int size);            // workgroups that share a row of such values
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t stream, const KTimer& tm);
 

@@ -34,7 +34,7 @@ namespace {
 
 typedef unsigned long long u64;
 constexpr int kBeamThreads = 64 * kBeamWaves;
-constexpr int kListCap = LORA_MAX_BEAMS + 64 * 8;   // a list's `best` and one load of every lane
+constexpr int kListCap = 2 * LORA_MAX_BEAMS + 64 * 8;   // a list before it is cut back, and one load of every lane
 constexpr float kLog2e = 1.44269504088896341f;
 
 struct Entry {   // a candidate of the join
@@ -127,8 +127,34 @@ __device__ __forceinline__ int above(const u64* list, int n, u64 mine) {
   return place;
 }
 
-// Cut a wave's list of n entries back to its `best` largest, in order, with zeros behind them; returns their number.
+// Cut a wave's list of n entries back to its `best` largest, in order, with zeros behind them; returns their number.  Every
+// entry is counted against all: of a long list first those whose value is below the best-th largest go (250 entries: 3 us
+// without).
 __device__ __forceinline__ int cut_list(u64* list, u64* sorted, int n, int best, int lane) {
+  if (n > 2 * LORA_MAX_BEAMS) {
+    constexpr int kHold = kListCap / 64;
+    uint32_t value[kHold], floor_ = 0;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) value[k] = k * 64 + lane < n ? (uint32_t)(list[k * 64 + lane] >> 24) : 0u;
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t test = floor_ | 1u << bit;
+      int count = 0;
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) count += __popcll(__ballot(value[k] >= test));
+      if (count >= best) floor_ = test;
+    }
+    int left = 0;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {   // places that have been read are written
+      const u64 mask = __ballot(value[k] >= floor_);
+      const u64 e = list[k * 64 + lane];
+      wave_lds_sync();
+      if (value[k] >= floor_) list[left + __popcll(mask & ((1ull << lane) - 1ull))] = e;
+      left += __popcll(mask);
+    }
+    n = left;
+  }
   if (lane < kAhead) list[n + lane] = 0;
   wave_lds_sync();
   for (int i = lane; i < n; i += 64) {
@@ -142,6 +168,22 @@ __device__ __forceinline__ int cut_list(u64* list, u64* sorted, int n, int best,
   if (lane < kAhead) list[n + lane] = 0;
   wave_lds_sync();
   return n;
+}
+
+// the want-th largest of the workgroup's values, N a thread, or 0; sums: LDS
+template <int N> __device__ __forceinline__ uint32_t nth_of_group(const uint32_t (&values)[N], int want, uint32_t (&sums)[2][kBeamWaves], int lane, int w) {
+  uint32_t at = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t test = at | 1u << bit;
+    int count = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) count += __popcll(__ballot(values[k] >= test));
+    if (lane == 0) sums[bit & 1][w] = (uint32_t)count;
+    __syncthreads();
+    if ((int)(sums[bit & 1][0] + sums[bit & 1][1] + sums[bit & 1][2] + sums[bit & 1][3]) >= want) at = test;
+  }
+  return at;
 }
 
 }  // namespace
@@ -241,7 +283,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
             if (hit) list[n + __popcll(mask & ((1ull << lane) - 1ull))] = key_of(beam, v, ((tile * U + u) * 64 + lane) * N + e - shift);
             n += __popcll(mask);
           }
-          if (n > LORA_MAX_BEAMS) {   // room for another load; tokens to come are higher, so equal values no longer enter
+          if (n > max(LORA_MAX_BEAMS, 2 * best)) {   // room for another load; tokens to come are higher, so equal values no longer enter
             n = cut_list(list, sorted, n, best, lane);
             if (n == best) floor_ = unordered(ordered(key_value(list[best - 1])) + 1u);
           }
@@ -285,13 +327,17 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   // ---- the request's join
   __shared__ float score_s[LORA_MAX_BEAMS], weight_s[LORA_MAX_BEAMS];
   __shared__ int over_s[LORA_MAX_BEAMS];   // 0: read, 1: ended, 2: gives no candidate
-  __shared__ uint32_t floors_s[kBeamWaves];
+  __shared__ uint32_t floors_s[2][kBeamWaves];
   constexpr int kFetch = 4, kEntries = LORA_MAX_BEAMS * (2 + kFetch * kBeamWaves);   // ended beams, those kept, new ones
+  constexpr int kLists = (kBeamMaxLists + kBeamThreads - 1) / kBeamThreads;
   static_assert(sizeof(Entry) * (kEntries + kAhead + LORA_MAX_BEAMS) <= sizeof(lists), "the lists' LDS holds the join's");
   Entry *entries = reinterpret_cast<Entry*>(&lists[0][0]), *sorted = entries + kEntries + kAhead;
-  const int row0 = request * a.beams, per_row = a.segs * best, n = a.beams * per_row;
-  const auto fetch = [&](int i) { return i < n ? get_word(a.keys + (size_t)row0 * per_row + i) : 0; };
-  u64 key[kFetch];   // of a row that was not read: what an earlier call left, and not taken
+  const int row0 = request * a.beams, lists_n = a.beams * a.segs, n = lists_n * best;
+  // (2048 of 64 lists: 50 us in rounds of all, 60 list by list; 65536 of 1024: 6200 and 100)
+  const bool many = n > 2 * kFetch * kBeamThreads;
+  const u64* const keys = a.keys + (size_t)row0 * a.segs * best;   // of a row that was not read: what an earlier call left, and not taken
+  u64 key[kFetch];   // the first of all candidates, unless they are many
+  const auto fetch = [&](int i) -> u64 { return !many && i < n ? get_word(keys + i) : 0; };
 #pragma unroll
   for (int k = 0; k < kFetch; ++k) key[k] = fetch(k * kBeamThreads + tid);
   // the rows' log sums, kRows of a wave's at a time
@@ -341,41 +387,43 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     const int j = key_row(k);
     return over_s[j] == 1 ? (double)score_s[j] : (double)score_s[j] + ((double)key_value(k) - lse_s[j]);
   };
-  // kFetch candidates a thread and round.  Those of the best-th largest of a wave's lanes' own best and above come on the
-  // list, at most kFetch for each of `best` lanes a wave, and the list is cut back to `best`.
-  for (int i0 = 0; i0 < n; i0 += kFetch * kBeamThreads) {
-    u64 next[kFetch];
+  // a candidate, and its rank rounded down as an ordered integer; 0: none
+  const auto ranked = [&](u64 k, int beam_, Entry& e) -> uint32_t {
+    e = Entry{-INFINITY, k};
+    if (k == 0 || over_s[beam_] != 0) return 0;
+    const double s = candidate(k);
+    e.rank = s * (double)weight_s[key_row(k)];
+    return s > -INFINITY && e.rank == e.rank ? ordered(__double2float_rd(e.rank)) : 0;
+  };
+  const auto take = [&](const Entry& e, bool pass) {
+    const u64 mask = __ballot(pass);
+    if (mask == 0) return;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&count_s, __popcll(mask));
+    at = __shfl(at, 0) + __popcll(mask & ((1ull << lane) - 1ull));
+    if (pass) entries[at] = e;
+  };
+  // the list cut back to its `best`, in order; returns their number.  As in cut_list, a long one first to those that can be
+  // among them (1000 entries: 50 us without)
+  const auto cut = [&]() -> int {
+    __syncthreads();
+    int c = count_s;
+    if (c > 2 * LORA_MAX_BEAMS) {
+      constexpr int kHold = (kEntries + kBeamThreads - 1) / kBeamThreads;
+      uint32_t down[kHold];
 #pragma unroll
-    for (int k = 0; k < kFetch; ++k) next[k] = fetch(i0 + (kFetch + k) * kBeamThreads + tid);
-    Entry e[kFetch];
-    uint32_t down[kFetch], mine = 0;   // ranks rounded down, as ordered integers; 0: no candidate
-#pragma unroll
-    for (int k = 0; k < kFetch; ++k) {
-      e[k] = Entry{-INFINITY, key[k]};
-      down[k] = 0;
-      if (key[k] != 0 && over_s[(unsigned)(i0 + k * kBeamThreads + tid) / (unsigned)per_row] == 0) {
-        const double s = candidate(key[k]);
-        e[k].rank = s * (double)weight_s[key_row(key[k])];
-        if (s > -INFINITY && e[k].rank == e[k].rank) down[k] = ordered(__double2float_rd(e[k].rank));
+      for (int k = 0; k < kHold; ++k) down[k] = k * kBeamThreads + tid < c ? ordered(__double2float_rd(entries[k * kBeamThreads + tid].rank)) : 0u;
+      const uint32_t floor_ = nth_of_group(down, best, floors_s, lane, w);
+      if (tid == 0) count_s = 0;
+#pragma unroll 1
+      for (int i0 = 0; i0 < c; i0 += kBeamThreads) {   // places that have been read are written
+        const Entry e = entries[i0 + tid];
+        __syncthreads();
+        take(e, i0 + tid < c && ordered(__double2float_rd(e.rank)) >= floor_);
       }
-      mine = max(mine, down[k]);
-      key[k] = next[k];
+      __syncthreads();
+      c = count_s;
     }
-    const uint32_t least = nth_of_lanes(mine, best);
-    if (lane == 0) floors_s[w] = least;
-    __syncthreads();
-    const uint32_t floor_ = max(max(max(floors_s[0], floors_s[1]), max(floors_s[2], floors_s[3])), 1u);
-#pragma unroll
-    for (int k = 0; k < kFetch; ++k) {
-      const u64 mask = __ballot(down[k] >= floor_);
-      if (mask == 0) continue;
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&count_s, __popcll(mask));
-      at = __shfl(at, 0) + __popcll(mask & ((1ull << lane) - 1ull));
-      if (down[k] >= floor_) entries[at] = e[k];
-    }
-    __syncthreads();
-    const int c = count_s;
     if (tid < kAhead) entries[c + tid] = Entry{-INFINITY, 0};   // below every other
     __syncthreads();
     for (int i = tid; i < c; i += kBeamThreads) {
@@ -395,7 +443,81 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     if (tid < kept) entries[tid] = sorted[tid];
     if (tid == 0) count_s = kept;
     __syncthreads();
+    return kept;
+  };
+  if (!many) {
+    // A round of kFetch a thread: those of the best-th largest of a wave's lanes' own best and above come on the list, at most
+    // kFetch for each of `best` lanes a wave.
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kFetch * kBeamThreads) {
+      if (i0 > 0) (void)cut();
+      Entry e[kFetch];
+      uint32_t down[kFetch], mine = 0;
+#pragma unroll
+      for (int k = 0; k < kFetch; ++k) {
+        const int i = i0 + k * kBeamThreads + tid;
+        down[k] = ranked(key[k], min(i / (a.segs * best), a.beams - 1), e[k]);
+        mine = max(mine, down[k]);
+        key[k] = fetch(i + kFetch * kBeamThreads);
+      }
+      const uint32_t least = nth_of_lanes(mine, best);
+      if (lane == 0) floors_s[0][w] = least;
+      __syncthreads();
+      const uint32_t floor_ = max(max(max(floors_s[0][0], floors_s[0][1]), max(floors_s[0][2], floors_s[0][3])), 1u);
+#pragma unroll
+      for (int k = 0; k < kFetch; ++k) take(e[k], down[k] >= floor_);
+    }
+  } else {
+    // Many lists, each in order: kFetch of each at a time (and thread: where the lists are fewer several have one), and of a
+    // list no more once one is below the floor: at first the value
+    // that lists_best lists reach with their q-th, so that there are `best` candidates above it, then the last of the list
+    // whenever that is cut back.
+    const int q = (best + lists_n - 1) / lists_n, lists_best = (best + q - 1) / q;
+    Entry e, last{};
+    uint32_t at[kLists], floor_ = 0;
+    const auto list_beam = [&](int i) { return min(i / a.segs, a.beams - 1); };
+#pragma unroll
+    for (int j = 0; j < kLists; ++j) {
+      const int i = j * kBeamThreads + tid;
+      at[j] = ranked(i < lists_n ? get_word(keys + (size_t)i * best + (q - 1)) : 0, list_beam(i), e);
+    }
+    floor_ = max(nth_of_group(at, lists_best, floors_s, lane, w), 1u);
+    bool full = false;
+    unsigned open = ~0u;   // lists of this thread that go on, as bits
+    int side = 0;          // threads of a list, as a power of two
+    while (lists_n << (side + 1) <= kBeamThreads) ++side;
+    for (int e0 = 0; e0 < best && __syncthreads_or(open != 0); e0 += kFetch << side) {
+#pragma unroll 1
+      for (int i0 = 0, bit = 0; i0 < kLists * kBeamThreads; i0 += kBeamThreads, ++bit) {
+        const int i = (i0 + tid) >> side, at_list = e0 + (tid & ((1 << side) - 1)) * kFetch;
+        if (i >= lists_n) open &= ~(1u << bit);
+        if (i0 >= lists_n << side) continue;
+        u64 next[kFetch];
+#pragma unroll
+        for (int k = 0; k < kFetch; ++k) {
+          next[k] = 0;
+          if ((open >> bit & 1) && at_list + k < best) next[k] = get_word(keys + (size_t)i * best + at_list + k);
+        }
+        __syncthreads();
+        const int c = count_s;
+        __syncthreads();
+        if (c + kFetch * kBeamThreads > kEntries && cut() == best) {
+          full = true;
+          last = entries[best - 1];
+          floor_ = max(floor_, ordered(__double2float_rd(last.rank)));
+        }
+        uint32_t down = 0;
+#pragma unroll
+        for (int k = 0; k < kFetch; ++k) {
+          down = ranked(next[k], list_beam(i), e);
+          take(e, down >= floor_ && (!full || e.rank > last.rank || (e.rank == last.rank && e.key > last.key)));
+        }
+        if (down < floor_) open &= ~(1u << bit);
+      }
+      open &= (1u << kLists) - 1u;
+    }
   }
+  (void)cut();
   const int found = count_s;
   if (tid < best) {
     const int out = request * best + tid;

@@ -274,6 +274,7 @@ static void shape_walk() {
     const int segs = rax::beam_segs(rows, vocab, size);
     const long long tiles = ((long long)vocab * size + 15 + rax::kBeamTileBytes - 1) / rax::kBeamTileBytes;
     TRUE(segs >= 1 && (segs - 1) * (long long)rax::kBeamWaves < tiles);
+    TRUE((long long)std::min<long long>(rows, LORA_MAX_BEAMS) * segs <= rax::kBeamMaxLists);   // of a request
     if (segs > 1) TRUE(rows * segs * rax::kBeamWaves <= 3LL * rax::kBeamMaxWaves + rows * rax::kBeamWaves);
   }
 }
