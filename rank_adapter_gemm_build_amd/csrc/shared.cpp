@@ -181,10 +181,20 @@ lora_status lora_shared_attention(const lora_shared* attention, const void* q, i
   const long long seq_rows = ((long long)num_tokens + num_seqs - 1) / num_seqs * a.group_size;
   const long long group_rows = ((long long)num_tokens + std::max(1, num_groups) - 1) / std::max(1, num_groups) * a.group_size;
   const bool many = seq_rows > 16;
-  s.own_line = many ? line_shape(a, 2, 2, num_seqs, 6) : line_shape(a, 1, 0, num_seqs, 4);
-  // above kWideGroups groups their tables do not fit into LDS beside the tiles
-  const bool wide = group_rows > 64 && dtype == LORA_BF16 && (attention->dim == 64 || attention->dim == 128) && num_groups <= rax::kWideGroups;
+  // Above 128 dims a wave has one row tile: with two the registers spill, and a wait for them waits for the stores
+  // before (16 heads of 192, 64 rows a kv head over 8000 common tokens, fp32 366 -> 182 us, bf16 88 -> 81; 20 rows over 100
+  // common tokens 105 -> 26 and 39 -> 18; where the products count it costs: prompts of 500 tokens in bf16 365 -> 377).
+  const bool large = attention->dim > 128;
+  // Own keys are few as a rule: with up to 16 rows a wave has its own share and no join in the workgroup.
+  s.own_line = !many ? line_shape(a, 1, 0, num_seqs, 4) : large ? line_shape(a, 1, 2, num_seqs, 5) : line_shape(a, 2, 2, num_seqs, 6);
+  // Wide blocks for more rows than one of them holds, of 8-bit cells for more than two (heads of 128; blocks of 64 and wide,
+  // us: 128 rows over 8000 tokens 28 and 33, 132 rows 34 and 32, 256 rows 46 and 37, 1024 over 32000 351 and 251; e4m3, 4 groups
+  // over 4000: 192 rows 53 and 62, 256 rows 65 and 65, 512 rows 109 and 94).  Above kWideGroups groups their tables do not fit
+  // into LDS beside the tiles.
+  const bool wide = group_rows > (cache->dtype == LORA_FP8E4M3 ? 256 : 128) && dtype == LORA_BF16 &&
+                    (attention->dim == 64 || attention->dim == 128) && num_groups <= rax::kWideGroups;
   s.common_line = wide ? line_shape(a, 1, 4, num_groups, rax::kWideRowsLog2)
+                       : large ? line_shape(a, 1, 2, num_groups, 5)
                        : many || group_rows > 32 ? line_shape(a, 2, 2, num_groups, 6) : line_shape(a, 2, 1, num_groups, 5);
   if (s.own_line.step_log2 < 0 || s.common_line.step_log2 < 0)
     return fail(LORA_ERR_SHAPE, "num_tokens %d times %d query heads is too much for one call", num_tokens, attention->q_heads);

@@ -228,7 +228,12 @@ template <typename C, int DB> static void launch_shared_lines(const SharedArgs& 
       return;
     }
   }
-  if (s.own_line.row_tiles == 2) launch_shared_shape<C, DB, 2, 2, 2, 2, false>(s, stream, tm);
+  if constexpr (DB > 128) {
+    if (s.own_line.row_waves == 2) launch_shared_shape<C, DB, 1, 2, 1, 2, false>(s, stream, tm);
+    else if (once) launch_shared_shape<C, DB, 1, 0, 1, 2, true>(s, stream, tm);
+    else launch_shared_shape<C, DB, 1, 0, 1, 2, false>(s, stream, tm);
+    return;
+  } else if (s.own_line.row_tiles == 2) launch_shared_shape<C, DB, 2, 2, 2, 2, false>(s, stream, tm);
   else if (s.common_line.row_waves == 2 && once) launch_shared_shape<C, DB, 1, 0, 2, 2, true>(s, stream, tm);
   else if (s.common_line.row_waves == 2) launch_shared_shape<C, DB, 1, 0, 2, 2, false>(s, stream, tm);
   else if (once) launch_shared_shape<C, DB, 1, 0, 2, 1, true>(s, stream, tm);

@@ -255,7 +255,10 @@ static void shape_walk() {
     const rax::SharedArgs& s = g_shared;
     const bool wide = s.common_line.row_waves == 4;
     if (wide) TRUE(s.common_line.rows_log2 == rax::kWideRowsLog2 && ng <= rax::kWideGroups && type != 2 && (dim == 64 || dim == 128));
-    TRUE((s.own_line.row_waves == 0) == (s.own_line.row_tiles == 1) && s.own_line.rows_log2 == (s.own_line.row_waves == 0 ? 4 : 6));
+    for (const rax::LineShape* l : {&s.common_line, &s.own_line}) {
+      TRUE(1 << l->rows_log2 == (l == &s.common_line && wide ? 128 : 16 * l->row_tiles * std::max(1, l->row_waves)));
+      if (dim > 128) TRUE(l->row_tiles == 1 && (l->row_waves == 2 || (l == &s.own_line && l->row_waves == 0)));
+    }
     TRUE(s.own_line.min_steps >= 1 && s.common_line.min_steps >= 1 && s.a.workers % (2 * rax::kDies) == 0);
     // two tiles of keys and values, or the join's rows: at most 4 waves' 16 rows of 128 + 4 numbers and their statistics
     const long long lds = wide ? 4LL * 64 * dim * 2 : 4 * 16 * (128 + 4 + 4) * 4;
