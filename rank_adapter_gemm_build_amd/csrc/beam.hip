@@ -19,7 +19,9 @@
 // than its exponentials.
 //
 // What bounds it: reading the logits; next to that the exponential, 4 of some 12 vector
-// cycles a value.
+// cycles a value; then the join, 8 to 10 us of one workgroup a request.  Measured: 64 requests of 8 beams over
+// 128000 tokens in bf16 38 us (3.4 TB/s; reading alone 22), 24 of 6 over 50001 in fp32 with 12 candidates
+// 21, 1 of 4 over 32000 10.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>

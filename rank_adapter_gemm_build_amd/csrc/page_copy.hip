@@ -2,7 +2,8 @@
 //
 // What bounds it: memory, each cell read and written once.  A workgroup takes one page of keys or
 // of values of one layer, or where those are few and large every gridDim.z-th slab of one, 16 bytes a lane and load, in the order in which the cells lie (heads
-// inside tokens or tokens inside heads), with the loads of kCopyBatch chunks on the way together.
+// inside tokens or tokens inside heads), with the loads of kCopyBatch chunks on the way together.  Measured: 448 pages of
+// 16 tokens in 32 layers 170 us (5.6 TB/s read and written), 200 of 64 in e4m3 in 8 layers 73 (5.8), 3 in 32 layers 4.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
