@@ -686,7 +686,7 @@ lora_status lora_page_copy(int device, const lora_kv_cache* layers, int num_laye
 /*
  * Shared attention for up to max_seqs sequences and max_tokens new tokens (owns the workspace: the two results
  * of every row, 8 bytes * max_tokens * num_q_heads * (head_dim + 2), partial results of 768 KiB a head_dim value
- * on 256 compute units, and 48 bytes * max_seqs).  Arguments and errors of create as lora_attention_create.
+ * on 256 compute units, and 32 bytes * max_seqs).  Arguments and errors of create as lora_attention_create.
  */
 typedef struct lora_shared lora_shared;
 lora_status lora_shared_create(lora_shared** out, int device, int max_seqs, int max_tokens,
