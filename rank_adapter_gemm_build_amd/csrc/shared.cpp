@@ -187,15 +187,18 @@ lora_status lora_shared_attention(const lora_shared* attention, const void* q, i
   const bool large = attention->dim > 128;
   // Own keys are few as a rule: with up to 16 rows a wave has its own share and no join in the workgroup.
   s.own_line = !many ? line_shape(a, 1, 0, num_seqs, 4) : large ? line_shape(a, 1, 2, num_seqs, 5) : line_shape(a, 2, 2, num_seqs, 6);
-  // Wide blocks for more rows than one of them holds, of 8-bit cells for more than two (heads of 128; blocks of 64 and wide,
-  // us: 128 rows over 8000 tokens 28 and 33, 132 rows 34 and 32, 256 rows 46 and 37, 1024 over 32000 351 and 251; e4m3, 4 groups
-  // over 4000: 192 rows 53 and 62, 256 rows 65 and 65, 512 rows 109 and 94).  Above kWideGroups groups their tables do not fit
-  // into LDS beside the tiles.
+  // Wide blocks for more rows than one of them holds, of 8-bit cells for more than two (heads of 128; blocks of 32 and wide, us:
+  // 96 rows over 8000 tokens 28 and 31, but in 8 groups over 4000 76 and 65; 132 rows 30 and 32, and 112 and 83; 256 rows 45 and
+  // 36; 1024 over 32000 363 and 266; e4m3, 4 groups over 4000: 192 rows 52 and 62, 256 rows 58 and 64, 512 rows 102 and 95).
+  // Above kWideGroups groups their tables do not fit into LDS beside the tiles.
   const bool wide = group_rows > (cache->dtype == LORA_FP8E4M3 ? 256 : 128) && dtype == LORA_BF16 &&
                     (attention->dim == 64 || attention->dim == 128) && num_groups <= rax::kWideGroups;
+  // Else blocks of 32 whose waves split the keys, of 64 and two such pairs for many rows in fp32, where their products bind
+  // (16 groups over 3000 tokens, heads of 128, blocks of 32 and of 64, us: bf16 36 rows 58 and 68, 64 rows 63 and 70, 128 rows 101
+  // and 105; fp32 165 and 156, 176 and 158, 304 and 292).  Where sequences have many rows both lines have the same shape.
   s.common_line = wide ? line_shape(a, 1, 4, num_groups, rax::kWideRowsLog2)
                        : large ? line_shape(a, 1, 2, num_groups, 5)
-                       : many || group_rows > 32 ? line_shape(a, 2, 2, num_groups, 6) : line_shape(a, 2, 1, num_groups, 5);
+                       : many || (dtype == LORA_F32 && group_rows > 32) ? line_shape(a, 2, 2, num_groups, 6) : line_shape(a, 2, 1, num_groups, 5);
   if (s.own_line.step_log2 < 0 || s.common_line.step_log2 < 0)
     return fail(LORA_ERR_SHAPE, "num_tokens %d times %d query heads is too much for one call", num_tokens, attention->q_heads);
   // own keys that one block of rows reads, in whole 128-byte lines, need no place in the caches

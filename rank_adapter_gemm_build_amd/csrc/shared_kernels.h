@@ -238,12 +238,19 @@ template <typename C, int DB> static void launch_shared_lines(const SharedArgs& 
     if (s.own_line.row_waves == 2) launch_shared_shape<C, DB, 1, 2, 1, 2, false>(s, stream, tm);
     else if (once) launch_shared_shape<C, DB, 1, 0, 1, 2, true>(s, stream, tm);
     else launch_shared_shape<C, DB, 1, 0, 1, 2, false>(s, stream, tm);
-    return;
-  } else if (s.own_line.row_tiles == 2) launch_shared_shape<C, DB, 2, 2, 2, 2, false>(s, stream, tm);
-  else if (s.common_line.row_waves == 2 && once) launch_shared_shape<C, DB, 1, 0, 2, 2, true>(s, stream, tm);
-  else if (s.common_line.row_waves == 2) launch_shared_shape<C, DB, 1, 0, 2, 2, false>(s, stream, tm);
-  else if (once) launch_shared_shape<C, DB, 1, 0, 2, 1, true>(s, stream, tm);
-  else launch_shared_shape<C, DB, 1, 0, 2, 1, false>(s, stream, tm);
+  }
+  if constexpr (sizeof(C) == 4 && DB <= 128) {
+    if (s.common_line.row_waves == 2 && s.own_line.row_tiles == 1) {
+      if (once) launch_shared_shape<C, DB, 1, 0, 2, 2, true>(s, stream, tm);
+      else launch_shared_shape<C, DB, 1, 0, 2, 2, false>(s, stream, tm);
+      return;
+    }
+  }
+  if constexpr (DB <= 128) {
+    if (s.own_line.row_tiles == 2) launch_shared_shape<C, DB, 2, 2, 2, 2, false>(s, stream, tm);
+    else if (once) launch_shared_shape<C, DB, 1, 0, 2, 1, true>(s, stream, tm);
+    else launch_shared_shape<C, DB, 1, 0, 2, 1, false>(s, stream, tm);
+  }
 }
 template <typename C> hipError_t launch_shared_of(const SharedArgs& s, hipStream_t stream, const KTimer& tm) {
   if (s.a.c.dim <= 64) launch_shared_lines<C, 64>(s, stream, tm);
