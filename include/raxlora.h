@@ -621,8 +621,8 @@ lora_status lora_beams_destroy(lora_beams* beams);
  * The best continuations of each request.  Row b = request * beams + beam has logits[b][0..vocab) (row
  * stride ldlogits, LORA_BF16 or LORA_F32) and the score scores[b] so far; its candidate of token v has the score
  *   s(b, v) = scores[b] + logits[b][v] - ln sum_u exp logits[b][u].
- * A row with ended[b] != 0 (ended may be NULL) has one candidate, end_token with the score scores[b], and its
- * logits are not read; nor are those of a row whose score is -inf or NaN, which has none.  Candidates rank by s, or by
+ * A row with ended[b] != 0 (ended may be NULL) has one candidate, end_token with the score scores[b], and its logits
+ * have no effect; nor have those of a row whose score is -inf or NaN, which has no candidate.  Candidates rank by s, or by
  * weights[b] s (weights may be NULL; a row whose weight is not above 0 has no candidates): the
  * larger first, of equal ones the lower row, within a row the larger logit, of equal ones the lower token.
  * Candidates whose score is -inf or NaN are not chosen (a logit of -inf; any of a row whose logits

@@ -172,3 +172,16 @@ def test_a_step_of_the_lines_equals_another_split():
         out, lse = call(tuple(case), hq, kv, dim)
         near_paged(tuple(case), hq, kv, dim, (1.0, 1.0), out, lse, f"{len(starts) - 1} groups")
         assert out.dtype is BF
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_many_wide_groups(cache):
+    """More groups than have even parts, so that shares begin and end anywhere in a unit; and as many as there may be."""
+    scales = (0.75, 1.5) if cache == "fp8" else (1.0, 1.0)
+    for groups, news, hq, kv, dim in (([(100 + 97 * g, [1 + (7 * g + i) % 40 for i in range(70)]) for g in range(24)], 1, 4, 1, 64),
+                                      ([(1 + 211 * g % 1500, [1 + i % 3 for i in range(66 + g)]) for g in range(17)], 1, 8, 2, 128),
+                                      ([(16 + g % 90, [70 + g % 5] * 2) for g in range(1024)], 35, 4, 1, 64)):
+        case = shared_case(len(groups), groups, news, hq, kv, dim, cache)
+        out, lse = call(case, hq, kv, dim, scales)
+        near_paged(case, hq, kv, dim, scales, out, lse, f"{len(groups)} wide groups {cache}")
+        assert torch.equal(out, call(case, hq, kv, dim, scales, lse=False)[0])
