@@ -10,6 +10,11 @@
 // term is then exactly 1, and lanes, waves and shares are joined in 64 bits, so the few terms
 // that make up a peaked distribution's sum carry no rounding of an exponential.  Scores are
 // formed in 64 bits: candidates of two beams may lie next to each other.
+// Equal terms after a larger one all round the same way, in every lane, so a lane's fp32 sum goes to 64 bits every
+// kBeamRun tiles.  In units of 2^-24 of the sum a run then has at most 32 from additions of loads and 7 from those within one,
+// about 3 for each move of its maximum, and a term d below the maximum 2.2 d + 2, of up to 65536 a lane 20 on average.
+// They cannot all be at their most (32 needs one large term, the others none), so the 2^-18 of the contract, 64 units,
+// hold for every vocabulary and number of rows.  (Without the runs: 2^-16 at 256 tiles a wave.)
 //
 // Lists.  A candidate is one 64-bit word that sorts as (row, value, token) do: complement of the
 // row, value as an ordered integer, complement of the token.  A wave appends to its list in LDS
@@ -38,6 +43,7 @@ typedef unsigned long long u64;
 constexpr int kBeamThreads = 64 * kBeamWaves;
 constexpr int kListCap = 2 * LORA_MAX_BEAMS + 64 * 8;   // a list before it is cut back, and one load of every lane
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr int kBeamRun = 8;   // tiles whose terms a lane adds in fp32
 
 struct Entry {   // a candidate of the join
   double rank;
@@ -250,9 +256,20 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
   const bool live = __builtin_amdgcn_readlane(over, beam) == 0;   // else the row is not read
   if (live) {
     u64 *list = lists[w], *sorted = list + kListCap + kAhead;
-    float m = -INFINITY, l = 0.f, floor_ = -FLT_MAX;
-    int n = 0;
+    float m = -INFINITY, l = 0.f, floor_ = -FLT_MAX, sum_m = -INFINITY;
+    double sum_l = 0.0;   // of the runs before, relative to sum_m
+    const auto end_run = [&] {
+      if (__any(sum_l != 0.0 && m != sum_m)) sum_l *= m == sum_m ? 1.0 : exp((double)sum_m - (double)m);
+      sum_l += (double)l;
+      sum_m = m;
+      l = 0.f;
+    };
+    int n = 0, run = 0;
     for (bool first = true; tile < tiles; tile += stride, first = false) {
+      if (run++ == kBeamRun) {
+        end_run();
+        run = 1;
+      }
       float top[U], all = -INFINITY;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -296,7 +313,8 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     n = cut_list(list, sorted, n, best, lane);
     // the wave's sum
     float top;
-    const double sum = joined_sum(m, (double)l, top);
+    end_run();
+    const double sum = joined_sum(m, sum_l, top);
     if (lane == 0) {
       counts[w] = n;
       put_word(a.sums + 2 * ((size_t)row * stride + tile0), (u64)__float_as_uint(top));
