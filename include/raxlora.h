@@ -623,7 +623,7 @@ lora_status lora_beams_destroy(lora_beams* beams);
  *   s(b, v) = scores[b] + logits[b][v] - ln sum_u exp logits[b][u].
  * A row with ended[b] != 0 (ended may be NULL) has one candidate, end_token with the score scores[b], and its logits
  * have no effect; nor have those of a row whose score is -inf or NaN, which has no candidate.  Candidates rank by s, or by
- * weights[b] s (weights may be NULL; a row whose weight is not above 0 has no candidates): the
+ * weights[b] s (weights may be NULL; a row whose weight is not above 0 has no candidates; +inf times 0 is taken as 0): the
  * larger first, of equal ones the lower row, within a row the larger logit, of equal ones the lower token.
  * Candidates whose score is -inf or NaN are not chosen (a logit of -inf; any of a row whose logits
  * hold NaN or +inf or are all -inf).

@@ -26,6 +26,7 @@ def select(logits, scores, beams, best, ended=None, end_token=-1, weights=None):
     """Per request the ranked candidates [(rank, row, token, score, ended)], at most `best` of them."""
     x = np.asarray(logits, dtype=np.float64)
     lse = log_sums(x)
+    rank = lambda s, w: s * w if s else 0.0  # noqa: E731  (infinity times 0 is taken as 0)
     out = []
     for r in range(x.shape[0] // beams):
         found = []
@@ -34,7 +35,7 @@ def select(logits, scores, beams, best, ended=None, end_token=-1, weights=None):
             if not c > -math.inf or not w > 0:
                 continue
             if ended is not None and ended[row]:
-                found.append((c * w, row, 0, int(end_token), c, 1))
+                found.append((rank(c, w), row, 0, int(end_token), c, 1))
                 continue
             if not math.isfinite(lse[row]):
                 continue
@@ -42,7 +43,7 @@ def select(logits, scores, beams, best, ended=None, end_token=-1, weights=None):
             for place, t in enumerate(order):
                 if x[row, t] > -math.inf:
                     s = c + (x[row, t] - lse[row])
-                    found.append((s * w, row, place, int(t), s, int(t == end_token)))
+                    found.append((rank(s, w), row, place, int(t), s, int(t == end_token)))
         found.sort(key=lambda f: (-f[0], f[1], f[2]))
         out.append([(f[0], f[1], f[3], f[4], f[5]) for f in found[:best]])
     return out

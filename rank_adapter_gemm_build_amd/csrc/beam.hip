@@ -49,6 +49,9 @@ struct Entry {   // a candidate of the join
   double rank;
   u64 key;
 };
+// A weight of infinity (above 0 as all are) times a score of 0 is taken as 0: every rank is a number, and within a row the
+// ranks keep the order of the scores.
+__device__ __forceinline__ double rank_of(double score, float weight) { return score == 0.0 ? 0.0 : score * (double)weight; }
 
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v);
@@ -399,7 +402,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     }
     // ended beams
     const u64 mask = __ballot(over == 1);
-    if (over == 1) entries[__popcll(mask & ((1ull << lane) - 1ull))] = Entry{(double)lane_score * (double)lane_weight, key_of(lane, 0.f, a.end_token)};
+    if (over == 1) entries[__popcll(mask & ((1ull << lane) - 1ull))] = Entry{rank_of((double)lane_score, lane_weight), key_of(lane, 0.f, a.end_token)};
     if (lane == 0) count_s = __popcll(mask);
   }
   __syncthreads();
@@ -412,8 +415,8 @@ __global__ __launch_bounds__(kBeamThreads) void beam_select_kernel(BeamArgs a) {
     e = Entry{-INFINITY, k};
     if (k == 0 || over_s[beam_] != 0) return 0;
     const double s = candidate(k);
-    e.rank = s * (double)weight_s[key_row(k)];
-    return s > -INFINITY && e.rank == e.rank ? ordered(__double2float_rd(e.rank)) : 0;
+    e.rank = rank_of(s, weight_s[key_row(k)]);
+    return s > -INFINITY ? ordered(__double2float_rd(e.rank)) : 0;
   };
   const auto take = [&](const Entry& e, bool pass) {
     const u64 mask = __ballot(pass);
