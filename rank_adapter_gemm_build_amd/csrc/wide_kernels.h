@@ -53,6 +53,15 @@ __device__ __forceinline__ u32x4_t cells_words(const char* base) {
   return u32x4_t{(uint32_t)uniform((int)(uint32_t)u), (uint32_t)uniform((int)((uint32_t)(u >> 32) & 0xffffu)), 0x7fffffffu, 0x00027000u};
 }
 
+// The rests of two weights (bf16, none negative), above 0 where the weights' upper parts are, so that times an infinity they add
+// nothing but that infinity; the rest of a weight of 0 stays 0.  (As integers bf16 numbers that are not negative keep their order.)
+__device__ __forceinline__ uint32_t above_zero(uint32_t rest, uint32_t upper) {
+  typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+  const u16x2_t least = {0x0da2, 0x0da2};   // 1e-30
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, rest),
+                                                                __builtin_elementwise_min(__builtin_bit_cast(u16x2_t, upper), least)));
+}
+
 template <typename C, int D, class Line>
 __device__ __forceinline__ void attend_wide(const AttentionArgs& a, const Line line, float4* lds, const int* sums, int b_, int work_, int workers_,
                                             int step_log2) {
@@ -281,8 +290,7 @@ __device__ __forceinline__ void attend_wide(const AttentionArgs& a, const Line l
             }
             const uint32_t u0 = __float_as_uint(e[0]), u1 = __float_as_uint(e[1]);
             hw[k] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
-            // above 0 wherever the weight is, so that times an infinity it adds nothing but that infinity
-            lw[k] = bf16_pair(fmaxf(e[0] - __uint_as_float(u0 & 0xffff0000u), 1e-30f), fmaxf(e[1] - __uint_as_float(u1 & 0xffff0000u), 1e-30f));
+            lw[k] = above_zero(bf16_pair(e[0] - __uint_as_float(u0 & 0xffff0000u), e[1] - __uint_as_float(u1 & 0xffff0000u)), hw[k]);
           }
         }
       // o += weights times values, 16 keys at a time; the reads of the next 16 go between the products of these
