@@ -40,12 +40,13 @@ typedef __attribute__((address_space(3))) i16x4_t lds_four;
 __device__ __forceinline__ lds_char* lds_at(void* p) { return (lds_char*)(__attribute__((address_space(3))) void*)p; }
 
 // 16 bytes of each lane from memory to LDS, at `to` on in order of the lanes.  The compiler is not told that LDS changes: it
-// would wait for the next tile before every read of this one.  Arrival is waited for by stores_done.  (m0 is set anew before
-// every use by the compiler itself.)
+// would wait for the next tile before every read of this one.  Arrival is waited for by stores_done.  m0, which holds the place in
+// LDS and is read when the load is issued, is left as it was: the compiler reserves it, and takes no note of its being changed.
 __device__ __forceinline__ void load_to_lds(u32x4_t r, uint32_t ofs, uint32_t sofs, lds_char* to) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :: "s"((uint32_t)(uintptr_t)to), "v"(ofs), "s"(r), "s"(sofs) : "memory");
+  uint32_t kept;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+               : "=&s"(kept) : "s"((uint32_t)(uintptr_t)to), "v"(ofs), "s"(r), "s"(sofs) : "memory");
 #endif
 }
 __device__ __forceinline__ u32x4_t cells_words(const char* base) {
