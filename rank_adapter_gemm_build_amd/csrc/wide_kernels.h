@@ -75,8 +75,8 @@ __device__ __forceinline__ void attend_wide(const AttentionArgs& a, const Line l
   const int tid = threadIdx.x, lane = lane_id(), w = uniform(tid >> 6), r32 = lane & 31, h = lane >> 5;
   const int ps = a.c.page_shift, max_len = a.max_pages << ps, group = a.group_size;
   const bool flip = a.scale < 0.f;                 // the products of -q: the scale is then positive
-  // above 0, so that a score of minus infinity stays one
-  const float qs = fmaxf(fabsf(a.scale) * a.c.k_scale * 1.44269504088896341f, 1.2e-38f);
+  // above 0, so that a score of minus infinity stays one; the least number above 0, times which no other score counts (below 2^-20)
+  const float qs = fmaxf(fabsf(a.scale) * a.c.k_scale * 1.44269504088896341f, 1.4e-45f);
   lds_char* const tiles = lds_at(lds);             // [2][K, V]
 
   // a lane's place in a tile: of its key's chunks; of the key and 4 dims that it supplies to a transposing read

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import test_gpu_kv as base
 from test_gpu_shared_attention import call, shared_case
 
 pytestmark = pytest.mark.gpu
@@ -27,3 +28,16 @@ def test_values_of_weight_0_have_no_effect(members, dim, low):
     assert got[0][0].isfinite().all() and got[0][0].abs().max() > 0.1
     for out, lse in got[1:]:
         assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-39, -1e-39, 1e-44, 2e-38])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("members", [3, 40])
+def test_scales_near_0(members, dim, scale):
+    """Products of queries and keys of up to some 1e37, which such scales take to less than 1 (0 to 0: every key counts alike)."""
+    case = shared_case(members, [(150, [1 + i % 30 for i in range(members)])], 1, 8, 2, dim, "bf16")
+    q, k, v, table, lens, starts, _, _ = case
+    q *= 1e18
+    k *= 1e17
+    out, lse = call(case, 8, 2, dim, scale=scale)
+    base.check_attend(q, k, v, table, lens, starts, 16, 8, 2, dim, out, lse, scale, 0, (1.0, 1.0), f"scale {scale} {members}x{dim}")
