@@ -632,7 +632,8 @@ lora_status lora_beams_destroy(lora_beams* beams);
  * end_token, else 0; for places without a candidate -1, -1, -inf, 0.
  * Exponentials are summed in fp32 relative to maxima kept by each lane (2^-18 of the sum at most, 2^-27 as a
  * rule), the rest and the scores that rank are in 64 bits, scores_out is rounded once.  The result is the same on every call.
- * With candidates = beams, scores_out may be scores and ended_out may be ended; else outputs overlap nothing.
+ * With candidates = beams, scores_out may be scores and ended_out may be ended; else outputs overlap nothing, the logits
+ * (from their first value to their last) among it.
  * end_token: in [0, vocab), or -1 for none where ended is NULL.  One launch on `stream`; two
  * calls on one object must not overlap in time.  Errors: INVALID_ARG (NULL, end_token, outputs that overlap), SHAPE
  * (num_requests < 0, ldlogits < vocab), CAPACITY (num_requests above the object's), DTYPE, ALIGN (logits).

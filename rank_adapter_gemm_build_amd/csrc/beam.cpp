@@ -110,7 +110,10 @@ lora_status lora_beam_select(const lora_beams* beams, const void* logits, int ld
   const size_t in = 4 * (size_t)num_requests * beams->beams, n = 4 * (size_t)num_requests * beams->candidates;
   const bool same = beams->beams == beams->candidates;   // a request's outputs then lie where its own inputs do
   const void* const outs[4] = {parents, tokens, scores_out, ended_out};
+  // one request's outputs are written while others' logits are read
+  const size_t rows = (size_t)num_requests * beams->beams, read = rows > 0 ? ((rows - 1) * ldlogits + beams->vocab) * size : 0;
   for (int i = 0; i < 4; ++i) {
+    if (overlap(outs[i], n, logits, read)) return fail(LORA_ERR_INVALID_ARG, "an output overlaps logits");
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i], n, outs[j], n)) return fail(LORA_ERR_INVALID_ARG, "two outputs overlap");
     const void* const ins[3] = {scores, ended, weights};
