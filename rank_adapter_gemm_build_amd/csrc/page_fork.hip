@@ -65,7 +65,7 @@ template <int T, int PER> __global__ __launch_bounds__(T) void page_fork_kernel(
   constexpr int C = kForkColumns, W = T / 64;
   // of an old row: its entries in the strip, its length, its first child, its number of granted children
   extern __shared__ int4 strip_s[];
-  __shared__ int part_s[2][W], refused_s, invalid_s, last_s;
+  __shared__ int part_s[2][W], invalid_s, last_s;
   const int R = a.rows, N = a.num_pages, ps = a.page_shift, tid = threadIdx.x, lane = tid & 63;
   int *len_s = reinterpret_cast<int*>(strip_s + R), *first_s = len_s + R, *kids_s = first_s + R;
   const bool first_wg = blockIdx.x == 0;
@@ -83,7 +83,7 @@ template <int T, int PER> __global__ __launch_bounds__(T) void page_fork_kernel(
     }
   }
   const int head = ring_head(a.cursor[0], N), free_pages = clamp_int(a.cursor[1], 0, N);
-  if (tid == 0) refused_s = invalid_s = 0;
+  if (tid == 0) invalid_s = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
     if (i < count) {
@@ -116,7 +116,7 @@ template <int T, int PER> __global__ __launch_bounds__(T) void page_fork_kernel(
   }
   for (int d = 32; d > 0; d >>= 1) longest = max(longest, __shfl_xor(longest, d));
   if (lane == 0) part_s[1][tid >> 6] = longest;
-  int needs, refused = 0, place = block_scan<W>(need, part_s[0], tid, needs);
+  int needs, place = block_scan<W>(need, part_s[0], tid, needs);
 #pragma unroll
   for (int v = 0; v < W; ++v) longest = max(longest, part_s[1][v]);
   const int taken = min(needs, free_pages);
@@ -127,7 +127,6 @@ template <int T, int PER> __global__ __launch_bounds__(T) void page_fork_kernel(
       if (place >= free_pages) {
         parent[i] = -1;
         size[i] = 0;
-        ++refused;
       }
       ++place;
     }
@@ -137,7 +136,6 @@ template <int T, int PER> __global__ __launch_bounds__(T) void page_fork_kernel(
       a.copy_tokens[r0 + i] = 0;
     }
   }
-  if (first_wg && refused) atomicAdd(&refused_s, refused);
   __syncthreads();
 
   // ---- strips of columns
