@@ -702,7 +702,11 @@ lora_status lora_shared_destroy(lora_shared* attention);
  * group's first sequence that does, and the other keys by the sequence's own.  A sequence that does not take part, one
  * outside of all groups and one with common_lens 0 are as in lora_paged_attention.  common_lens need
  * not be a multiple of the page size, nor all that the sequences share.  The result is bitwise the same on every call,
- * and that of lora_paged_attention but for rounding: all sums are fp32, with one rounding to out.
+ * and that of lora_paged_attention but for rounding: sums, maxima and products accumulate in fp32, 16-bit products take each weight in
+ * two bf16 parts (2^-16 of it), with one rounding to out.
+ * It takes two launches and some 14 us at least, lora_paged_attention one and 9.  Measured with 32 query and 8 kv heads of 128 it is
+ * the faster one from about 8000 common tokens on for two sequences, from 3000 for four, 1500 for eight, 700 for 16 and for
+ * several such groups; below, and for sequences with nothing in common, lora_paged_attention is the call to make.
  * group_start: device int32 [num_groups + 1], rising; values outside [0, num_seqs] are taken as the nearer
  * bound.  common_lens: device int32 [num_groups], taken as the nearer bound of [0, max_pages * page_size].  num_groups in
  * [0, max_seqs of the object].  Two launches on `stream`.  Two calls on one object must not overlap in time.

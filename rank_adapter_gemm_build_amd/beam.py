@@ -4,7 +4,7 @@ does between the logits and the next step's page plan, and the attention that re
     beams, plan, layers = Beams(device, requests, width, vocab), ForkPlan(device, rows, num_pages), KVLayers(caches)
     beam_select(beams, logits, scores, parents, tokens, scores)                           # once a step
     page_fork(plan, parents, lens, free_pages, cursor, shares, block_table, page_size)
-    page_copy(layers, plan.copy_src, plan.copy_dst, plan.copy_tokens)
+    page_copy(layers, plan.copy_src[:rows], plan.copy_dst[:rows], plan.copy_tokens[:rows])
     shared_attention(attention, q, cache, block_table, seq_lens, query_start, group_start, common_lens, out)   # per layer
 
 Imported by the package itself; argument checks and marshalling only."""
@@ -133,7 +133,8 @@ def page_fork(plan: ForkPlan, parents, lens, free_pages, cursor, shares, block_t
     """Block table rows continue the rows that `parents` names, with pages shared, copied where partly filled, and freed
     (see lora_page_fork).  parents, lens: int32 [rows], lens changes in place; free_pages: int32 ring [num_pages], cursor: int32
     [4], as page_plan takes them; shares: int32 [num_pages], holders of each page beyond the first.  The entries
-    of plan.copy_src, copy_dst and copy_tokens past the rows are left as they were."""
+    of plan.copy_src, copy_dst and copy_tokens past the rows are left as they were, with the pairs of an earlier call of more rows
+    among them: page_copy is given the first `rows` of each."""
     if kv.torch is None:
         kv._load()
     dev = plan.device
@@ -224,7 +225,7 @@ class SharedAttention:
 def shared_attention(attention: SharedAttention, q, cache: KVCache, block_table, seq_lens, query_start, group_start, common_lens, out,
                      scale: Optional[float] = None, lse=None, stream=None) -> None:
     """paged_attention of sequences whose first tokens lie in common pages, which are read once for all of a group (see
-    lora_shared_attention).  group_start: int32 [groups + 1], the first sequence of each group; common_lens: int32
+    lora_shared_attention, which also says from how many common tokens on that pays).  group_start: int32 [groups + 1], the first sequence of each group; common_lens: int32
     [groups], the tokens that its sequences have in common.  The other arguments are paged_attention's."""
     if kv.torch is None:
         kv._load()

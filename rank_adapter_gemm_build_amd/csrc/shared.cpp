@@ -188,8 +188,11 @@ lora_status lora_shared_attention(const lora_shared* attention, const void* q, i
   // Own keys are few as a rule: with up to 16 rows a wave has its own share and no join in the workgroup.
   s.own_line = !many ? line_shape(a, 1, 0, num_seqs, 4) : large ? line_shape(a, 1, 2, num_seqs, 5) : line_shape(a, 2, 2, num_seqs, 6);
   // Wide blocks for more rows than one of them holds, of 8-bit cells for more than two (heads of 128; blocks of 32 and wide, us:
-  // 96 rows over 8000 tokens 28 and 31, but in 8 groups over 4000 76 and 65; 132 rows 30 and 32, and 112 and 83; 256 rows 45 and
-  // 36; 1024 over 32000 363 and 266; e4m3, 4 groups over 4000: 192 rows 52 and 62, 256 rows 58 and 64, 512 rows 102 and 95).
+  // one group over 8000 tokens, 96 rows 35 and 33, 132 rows 37 and 39, 256 rows 57 and 43; over 32000 132 rows 104 and 85, 1024
+  // rows 363 and 266; 8 groups over 4000 112 rows 80 and 84, 132 rows 124 and 97, 256 rows 138 and 122; e4m3, 8 groups over 4000: 192
+  // rows 102 and 112, 260 rows 138 and 152, 320 rows 153 and 161, 384 rows 176 and 172, 512 rows 218 and 203; one over 8000: 320 rows
+  // 51 and 66, 512 rows 66 and 74; over 32000 141 and 126, 180 and 158 for 384 and 512).  Where few tokens are common blocks of 32
+  // stay ahead (200 tokens: 256 rows 20 and 26, e4m3 512 rows 30 and 34); the lengths are on the device, so the rule goes by rows.
   // Above kWideGroups groups their tables do not fit into LDS beside the tiles.
   const bool wide = group_rows > (cache->dtype == LORA_FP8E4M3 ? 256 : 128) && dtype == LORA_BF16 &&
                     (attention->dim == 64 || attention->dim == 128) && num_groups <= rax::kWideGroups;

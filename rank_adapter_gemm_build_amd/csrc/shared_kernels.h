@@ -16,7 +16,8 @@
 //
 // What bounds it: reading the keys and values once; with many rows the common line's products.  Measured (32 query and 8 kv
 // heads of 128, both launches): 4 sequences with 704 common tokens 17 us; 24 groups of 8 with 1000 to 6000 in e4m3 80 (bytes
-// 39); 64 sequences with 8000 70 (26); 256 with 32000 388 (206).
+// 39); 64 sequences with 8000 69 to 72 (26); 256 with 32000 390 to 399 (206).  With wide blocks and heads of 128 registers spill in
+// e4m3 (17 to 19) and, where sequences have many rows, in bf16 (30).
 #pragma once
 
 #include "attention_kernels.h"

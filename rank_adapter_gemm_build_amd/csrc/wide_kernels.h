@@ -15,8 +15,9 @@
 // go from memory to LDS directly; 8-bit ones are widened on the way.
 //
 // Measured, bf16, 1024 rows a kv head over 32000 keys: 255 us, 0.53 PFLOP/s of the products needed, 0.8 of those done, at
-// 1.6 to 1.8 GHz, which this load lets the chip run at.  Of a wave's 4800 cycles a tile 1500 go by before the tile is there, 670
-// in the first product, 1450 in the exponentials, 1130 in the second product; the other wave of the SIMD works meanwhile, so the
+// 1.6 to 1.8 GHz, which this load lets the chip run at.  Of a wave's 4800 cycles a tile 1500 go by before the tile is there (its
+// loads are issued late: a wave takes its page's id out of an array by its own number, and the compiler keeps that array in scratch, a
+// store and a load before the address is known), 670 in the first product, 1450 in the exponentials, 1130 in the second product; the other wave of the SIMD works meanwhile, so the
 // matrix cores are busy half of the time.  With each tile on its way for one and a half others, at two barriers a tile, 297 us.
 #pragma once
 
